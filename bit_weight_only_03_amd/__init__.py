@@ -63,6 +63,15 @@ _SIGS = {
     "w4a16_plan_variant": [_I, _I, _I, _I, _I, ctypes.c_char_p, _SZ],
     "w4a16_last_error": [],
 }
+# include/w8a8.h and include/tree_attn.h
+_L = ctypes.c_longlong
+_F = ctypes.c_float
+_SIGS_W8A8 = {
+    "w8a8_rmsnorm_quant": [_P, _I, _L, _P, _I, _P, _P, _I, _F, _P, _I, _P, _P, _I, _I, _P],
+    "w8a8_silu_mul_quant": [_P, _I, _L, _P, _I, _P, _P, _I, _I, _P],
+    "w8a8_workspace_bytes": [_I, _I, _I, _PSZ],
+    "w8a8_gemm": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _SZ, _P],
+}
 _STR_RESULT = ("w4a16_status_string", "w4a16_last_variant", "w4a16_last_error")
 
 _lib_handle = None
@@ -77,7 +86,7 @@ def _lib_get():
             raise ImportError(f"{LIB_PATH} is missing: build it with "
                               "`python -m bit_weight_only_03_amd.build`")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, args in _SIGS.items():
+        for name, args in (*_SIGS.items(), *_SIGS_W8A8.items()):
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = ctypes.c_char_p if name in _STR_RESULT else _I
@@ -93,6 +102,7 @@ class _LazyLib:
 _lib = _LazyLib()
 
 EXPORTED = tuple(_SIGS)
+EXPORTED_W8A8 = tuple(_SIGS_W8A8)
 
 
 def _ptr(t):
@@ -103,10 +113,27 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """torch's current HIP stream as an integer: 0.4 us through the raw query,
+    2.9 us through torch.cuda.current_stream(), which builds a Stream object."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if get and device:
+            _raw_stream = lambda: get(device())  # noqa: E731
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -285,3 +312,30 @@ def w4a16_bw_probe_sink_floats() -> int:
 
 def w4a16_bw_probe(buf, nbytes: int, sink, stream=None):
     _check("w4a16_bw_probe", _lib.w4a16_bw_probe(_ptr(buf), nbytes, _ptr(sink), _stream(stream)))
+
+
+def w8a8_rmsnorm_quant(x, x_dtype, ldx, residual, residual_dtype, h_out, weight, weight_dtype, eps,
+                       y_out, y_dtype, q, scales, M, K, stream=None):
+    _check("w8a8_rmsnorm_quant", _lib.w8a8_rmsnorm_quant(
+        _ptr(x), _dt(x_dtype), ldx, _ptr(residual), _dt(residual_dtype), _ptr(h_out), _ptr(weight),
+        _dt(weight_dtype), eps, _ptr(y_out), _dt(y_dtype), _ptr(q), _ptr(scales), M, K,
+        _stream(stream)))
+
+
+def w8a8_silu_mul_quant(x, x_dtype, ldx, y_out, y_dtype, q, scales, M, K, stream=None):
+    _check("w8a8_silu_mul_quant", _lib.w8a8_silu_mul_quant(
+        _ptr(x), _dt(x_dtype), ldx, _ptr(y_out), _dt(y_dtype), _ptr(q), _ptr(scales), M, K,
+        _stream(stream)))
+
+
+def w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
+    b = _SZ()
+    _check("w8a8_workspace_bytes", _lib.w8a8_workspace_bytes(M, N, K, ctypes.byref(b)))
+    return b.value
+
+
+def w8a8_gemm(x, x_scales, w, w_scales, y, y_dtype, M, N, K, workspace=None, workspace_bytes=0,
+              stream=None):
+    _check("w8a8_gemm", _lib.w8a8_gemm(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(y),
+                                       _dt(y_dtype), M, N, K, _ptr(workspace), workspace_bytes,
+                                       _stream(stream)))

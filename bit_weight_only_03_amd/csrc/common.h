@@ -304,6 +304,8 @@ struct Overrides {
     int w16_dot = -1;          // W16A16_DOT: 0 turns the W16 dot-product kernel off
     int w16_bal = -1;          // W16A16_BAL: 0 / 1 turns the W16 even-share kernel off / on where it fits
     int w16_split = 0;         // W16A16_SPLIT: K slices of the W16 tiled kernel
+    int w8_variant = -1;       // W8A8_VARIANT: kernel of the 8-bit product (make_plan's numbers)
+    int w8_split = 0;          // W8A8_SPLIT: its K slices
     long long w2t_staged_lds_max = 0;   // W2T_STAGED_LDS_MAX: LDS limit of the staged ternary kernel
 };
 const Overrides& overrides();

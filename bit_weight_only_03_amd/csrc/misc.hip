@@ -94,6 +94,8 @@ const Overrides& overrides() {
         geti("W16A16_DOT", o.w16_dot);
         geti("W16A16_BAL", o.w16_bal);
         geti("W16A16_SPLIT", o.w16_split);
+        geti("W8A8_VARIANT", o.w8_variant);
+        geti("W8A8_SPLIT", o.w8_split);
         if (const char* e = getenv("W2T_STAGED_LDS_MAX")) o.w2t_staged_lds_max = atoll(e);
     });
     return o;

@@ -1,0 +1,531 @@
+// w8a8_gemm.hip -- y = x . w^T for e4m3 operands with one fp32 scale per row
+// and 128 k of x and one per 128 x 128 block of w.
+//
+// Both operands come in rows of K bytes, and v_mfma_f32_16x16x128_f8f6f4 takes
+// exactly one scale block (128 k) of 16 rows of each: the block's sum leaves
+// the matrix unit in fp32 and takes its scales' product in one fp32 fma per
+// output.  w is the A operand and x the B operand, so a lane's four results
+// share one row m of x, hence one scale, and are four consecutive columns n
+// of y.
+//
+// Rows go to LDS by direct loads (buffer_load ... lds), 128 bytes of 8 rows
+// per instruction: whole cache lines, where the operand layout itself (16 rows
+// by 16 bytes for each quarter wave) would touch half lines.  A row's eight 16-byte
+// chunks are permuted by a key of the row on the way, so that the operand
+// reads (16 bytes at one chunk of 16 rows) are free of bank conflicts.
+//
+// Lane l of an operand holds row l & 15 and the chunks l >> 4 and 4 + (l >> 4)
+// of its 128 bytes.  Which k an MFMA slot stands for does not matter as long as
+// both operands agree.
+#include <atomic>
+
+#include "w8a8_common.h"
+
+using namespace w4k;
+
+namespace {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past every descriptor here: reads zeros
+constexpr int kStepK = 128;                  // k per step: one scale block, one MFMA
+constexpr int kMaxSplit = 64;
+constexpr int kMaxDynamicLds = 159 * 1024;   // a CU's 160 KiB less the kernels' static variables
+constexpr int kMaxDevices = 64;
+
+struct GemmArgs {
+    const uint8_t* x;
+    const float* x_scales;
+    const uint8_t* w;
+    const float* w_scales;
+    void* y;
+    float* part;          // fp32 partial sums of K slices
+    unsigned* counters;   // one per output tile, zero between calls
+    int y_dtype;
+    int M, N, K;
+    int kb;               // scale blocks of K
+    int S;                // K slices
+    int tiles_n, tiles_m;
+};
+
+__device__ __forceinline__ float4_t mfma_block(const i32x8_t& a, const i32x8_t& b) {
+    // Formats 0, 0: both e4m3.  Scale operands of constant 0 select the form without scales.
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, float4_t{0.f, 0.f, 0.f, 0.f}, 0, 0,
+                                                            0, 0, 0, 0);
+}
+
+// The operand whose row starts at p in LDS, chunks permuted with key.
+__device__ __forceinline__ i32x8_t operand(const uint8_t* p, int chunk, int key) {
+    const i32x4_t lo = *(const i32x4_t*)(p + 16 * (chunk ^ key));
+    const i32x4_t hi = *(const i32x4_t*)(p + 16 * ((chunk + 4) ^ key));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)to, 16, voff, soff, 0, 0);
+}
+
+// Four consecutive n of one row of y.  n and N are multiples of 4 and 8: a
+// quad is whole or absent.
+__device__ __forceinline__ void store4(const GemmArgs& a, int m, int n, const float* f) {
+    if (m >= a.M || n >= a.N) return;
+    const size_t o = (size_t)m * a.N + n;
+    if (a.y_dtype == W4A16_F32)
+        *(float4_t*)((float*)a.y + o) = float4_t{f[0], f[1], f[2], f[3]};
+    else if (a.y_dtype == W4A16_F16)
+        *(u32x2_t*)((uint16_t*)a.y + o) = u32x2_t{pk_f16(f[0], f[1]), pk_f16(f[2], f[3])};
+    else
+        *(u32x2_t*)((uint16_t*)a.y + o) = u32x2_t{pk_bf16(f[0], f[1]), pk_bf16(f[2], f[3])};
+}
+
+// The merge of K slices inside the launch.  Of every slice's workgroup the
+// first `threads` threads hold C partial sums each.  They store them
+// (coherently across the device, thread-contiguous); the workgroup
+// counts itself in, and the last to arrive adds all slices in slice order: the result does not depend on who was last.  True for that workgroup, whose
+// f then holds the sums.  No workgroup waits for another.
+template <int C>
+__device__ __forceinline__ bool merge_slices(const GemmArgs& a, int tile, int slice, int threads, bool live,
+                                             float* f) {
+    const int t = threadIdx.x;
+    float* const base = a.part + (size_t)tile * a.S * C * threads;
+    if (live) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            __hip_atomic_store(base + ((size_t)slice * C + c) * threads + t, f[c], __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __builtin_amdgcn_s_waitcnt(0);   // this thread's stores are done
+    __shared__ unsigned arrived;
+    __syncthreads();
+    if (t == 0) arrived = __hip_atomic_fetch_add(a.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrived != (unsigned)(a.S - 1)) return false;
+    if (t == 0) __hip_atomic_store(a.counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (live) {
+        float v[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = 0.f;
+        for (int s = 0; s < a.S; ++s)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                v[c] += __hip_atomic_load(base + ((size_t)s * C + c) * threads + t, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int c = 0; c < C; ++c) f[c] = v[c];
+    }
+    return true;
+}
+
+// ---- few rows ----
+//
+// Bound by one read of w.  A workgroup takes NT tiles of 16 columns and one
+// slice of K; its W waves take the slice's 128-k units in turn, each through
+// a private ring of RD slots in LDS ([16 NT rows of w][XR rows of x] x 128
+// bytes) that it fills RD units ahead and waits on alone: no barrier until the
+// waves' sums are added at the end.  MT tiles of 16 rows of x (XR = 8: half a
+// tile, whose other half repeats it and is not stored).
+constexpr int kTableFloats = 2048;   // products of scales a workgroup holds
+
+template <int MT, int XR, int NT, int RD, int W>
+__global__ __launch_bounds__(W * 64) void w8a8_skinny_kernel(GemmArgs a) {
+    constexpr int kSlot = (16 * NT + XR) * kStepK;
+    constexpr int kLoads = 2 * NT + XR / 8;
+    extern __shared__ uint8_t smem[];
+    float* const table = (float*)(smem + W * RD * kSlot);   // [unit of the slice][XR]
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
+
+    // Consecutive workgroups go to the XCDs in turn; the row blocks of one
+    // tile and slice sit 8 apart, on one XCD, whose L2 then serves w again.
+    const int r = blockIdx.x >> 3, mb = r % a.tiles_m, id = (r / a.tiles_m) * 8 + (blockIdx.x & 7);
+    if (id >= a.tiles_n * a.S) return;
+    const int tile = id / a.S, slice = id % a.S;
+    const int n0 = tile * 16 * NT, m0 = mb * XR;
+    const int b0 = (int)((long long)a.kb * slice / a.S), b1 = (int)((long long)a.kb * (slice + 1) / a.S);
+    const int units = b1 - b0, nu = units > wave ? (units - wave + W - 1) / W : 0;
+
+    // The products of scales of this slice, once: x_scales[b][m] w_scales[n/128][b].
+    constexpr int kPer = (kTableFloats + W * 64 - 1) / (W * 64);
+    float sx[kPer], sw[kPer];
+    const float* const ws = a.w_scales + (size_t)(n0 >> 7) * a.kb;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = i * W * 64 + t, u = e / XR, m = m0 + e % XR;
+        sx[i] = sw[i] = 0.f;
+        if (u < units && m < a.M) {
+            sx[i] = a.x_scales[(size_t)(b0 + u) * a.M + m];
+            sw[i] = ws[b0 + u];
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
+    const int rows_n = min(16 * NT, a.N - n0), rows_m = min(XR, a.M - m0);
+    const uint32_t K = a.K;
+    const uint8_t* const wp = a.w + (size_t)n0 * K;
+    const uint8_t* const xp = a.x + (size_t)m0 * K;
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(wp, rows_n * K), rx = make_rsrc(xp, rows_m * K);
+    const __amdgpu_buffer_rsrc_t none = make_rsrc(wp, 0);   // a unit that does not exist reads zeros
+    uint8_t* const ring = smem + wave * RD * kSlot;
+    const int row8 = lane >> 3, chunk = (lane & 7) ^ row8;   // slot chunk lane & 7 of row row8 holds this one
+    const uint32_t lane_off = row8 * K + 16u * chunk;
+    const int last = a.kb - 1, tail = (int)K - last * kStepK;   // bytes of the last unit's rows
+    const uint32_t tail_off = 16 * chunk < tail ? lane_off : kOutside;
+
+    auto issue = [&](int i) {
+        const int u = b0 + wave + i * W;
+        const bool there = i < nu;
+        const uint32_t off = u == last ? tail_off : lane_off;
+        const uint32_t k = (uint32_t)u * kStepK;
+        uint8_t* const slot = ring + (i % RD) * kSlot;
+#pragma unroll
+        for (int j = 0; j < 2 * NT; ++j) {
+            uint32_t o = off + 8u * j * K;
+            o = off == kOutside ? kOutside : o;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(there ? rw : none, (lds_ptr_t)(slot + j * 1024), 16, o, k, 0, kAuxNT);
+        }
+#pragma unroll
+        for (int j = 0; j < XR / 8; ++j) {
+            uint32_t o = off + 8u * j * K;
+            o = off == kOutside ? kOutside : o;
+            load_lds(there ? rx : none, slot + 16 * NT * kStepK + j * 1024, o, k);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < RD; ++i) issue(i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = i * W * 64 + t;
+        if (e < units * XR) table[e] = sx[i] * sw[i];
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+
+    float4_t acc[NT][MT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = float4_t{0.f, 0.f, 0.f, 0.f};
+    const int c = lane & 15, g = lane >> 4, key = c & 7;
+    for (int i = 0; i < nu; ++i) {
+        // All but the RD - 1 younger units' loads have arrived.
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((RD - 1) * kLoads) : "memory");
+        const uint8_t* const slot = ring + (i % RD) * kSlot;
+        i32x8_t wf[NT], xf[MT];
+        float s[MT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) wf[n] = operand(slot + (16 * n + c) * kStepK, g, key);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int row = XR == 8 ? c & 7 : 16 * m + c;
+            xf[m] = operand(slot + (16 * NT + row) * kStepK, g, key);
+            s[m] = table[(wave + i * W) * XR + row];
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot is read: it may be filled again
+        issue(i + RD);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float4_t d = mfma_block(wf[n], xf[m]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[n][m][q] = __builtin_fmaf(d[q], s[m], acc[n][m][q]);
+            }
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // no load may still be on its way into LDS
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+
+    // The waves' sums, added in wave order: [wave][tile][4][lane].
+    float* const red = (float*)smem;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) red[((wave * NT * MT + n * MT + m) * 4 + q) * 64 + lane] = acc[n][m][q];
+    __syncthreads();
+    constexpr int kTiles = NT * MT;
+    static_assert(kTiles <= W, "one operand tile per wave");
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    const int m = m0 + 16 * (wave % MT) + c, n = n0 + 16 * (wave / MT) + 4 * g;
+    const bool live = wave < kTiles && m < a.M && (XR != 8 || c < 8);
+    if (live) {
+#pragma unroll
+        for (int wv = 0; wv < W; ++wv)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) f[q] += red[((wv * kTiles + wave) * 4 + q) * 64 + lane];
+    }
+    if (a.S > 1 && !merge_slices<4>(a, tile * a.tiles_m + mb, slice, kTiles * 64, live, f)) return;
+    if (live) store4(a, m, n, f);
+}
+
+// ---- many rows ----
+//
+// Bound by the matrix units.  A workgroup of WGM x WGN waves takes BM rows of x
+// by BN rows of w; each step's 128 k of both go to one of two LDS buffers while
+// the other is multiplied, one barrier per step.
+//
+// Inside a wave's WN columns, row r of operand tile t is column
+// (r >> 2) WN/4 + 4 t + (r & 3): a lane's results over all tiles are then WN/4
+// consecutive columns of one row of y, stored 16 bytes at a time.  The key of
+// such a row follows r & 7, as its 8 neighbouring lanes need.
+template <int BM, int BN, int WGM, int WGN>
+__global__ __launch_bounds__(WGM * WGN * 64) void w8a8_tiled_kernel(GemmArgs a) {
+    constexpr int W = WGM * WGN, WM = BM / WGM, WN = BN / WGN, MT = WM / 16, NT = WN / 16;
+    constexpr int kBuf = (BM + BN) * kStepK;
+    constexpr int XL = BM / (8 * W), WL = BN / (8 * W);   // loads per wave and step
+    static_assert(XL >= 1 && WL >= 1 && WN <= 128 && WN >= 32, "tile shape");
+    extern __shared__ uint8_t smem[];
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
+    const int wm = wave % WGM, wn = wave / WGM;
+
+    // Tiles go to the XCDs in contiguous shares, each walked in columns of
+    // kGroup row tiles, so that an XCD's workgroups share rows of both operands in its L2.
+    constexpr int kGroup = 8;
+    const int total = a.tiles_m * a.tiles_n * a.S;
+    const int share = (total + 7) / 8;
+    const int id = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= share || id >= total) return;
+    const int slice = id % a.S, at = id / a.S;
+    const int band = at / (kGroup * a.tiles_n), in_band = at % (kGroup * a.tiles_n);
+    const int band_m = min(kGroup, a.tiles_m - band * kGroup);
+    const int tm = band * kGroup + in_band % band_m, tn = in_band / band_m;
+    const int m0 = tm * BM, n0 = tn * BN;
+    const int b0 = (int)((long long)a.kb * slice / a.S), b1 = (int)((long long)a.kb * (slice + 1) / a.S);
+
+    const uint32_t K = a.K;
+    const int rows_n = min(BN, a.N - n0), rows_m = min(BM, a.M - m0);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, rows_n * K);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)m0 * K, rows_m * K);
+    const int last = a.kb - 1, tail = (int)K - last * kStepK;
+    // Load j of a wave: rows 8 (j W + wave) + lane / 8.
+    const int row8 = lane >> 3;
+    const int wkey = (row8 & 3) | ((((8 * wave) / (WN / 4)) & 1) << 2);
+    static_assert((8 * W / (WN / 4)) % 2 == 0, "a wave's rows of w keep one key");
+    const int xchunk = (lane & 7) ^ row8, wchunk = (lane & 7) ^ wkey;
+    uint32_t xoff[XL], woff[WL];
+#pragma unroll
+    for (int j = 0; j < XL; ++j) xoff[j] = (uint32_t)(8 * (j * W + wave) + row8) * K + 16u * xchunk;
+#pragma unroll
+    for (int j = 0; j < WL; ++j) woff[j] = (uint32_t)(8 * (j * W + wave) + row8) * K + 16u * wchunk;
+
+    auto issue = [&](int b, uint8_t* buf) {
+        const uint32_t k = (uint32_t)b * kStepK;
+        const bool xout = b == last && 16 * xchunk >= tail, wout = b == last && 16 * wchunk >= tail;
+#pragma unroll
+        for (int j = 0; j < XL; ++j) load_lds(rx, buf + (j * W + wave) * 1024, xout ? kOutside : xoff[j], k);
+#pragma unroll
+        for (int j = 0; j < WL; ++j)
+            load_lds(rw, buf + BM * kStepK + (j * W + wave) * 1024, wout ? kOutside : woff[j], k);
+    };
+
+    const int c = lane & 15, g = lane >> 4, key = c & 7;
+    const int nw = n0 + wn * WN;   // this wave's first column; all of them in one scale block
+    const float* const ws = a.w_scales + (size_t)(min(nw, a.N - 1) >> 7) * a.kb;
+    int mrow[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) mrow[m] = min(m0 + wm * WM + 16 * m + c, a.M - 1);
+    float4_t acc[NT][MT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = float4_t{0.f, 0.f, 0.f, 0.f};
+
+    float sx[MT], sw;
+    auto scales = [&](int b) {
+        sw = ws[b];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) sx[m] = a.x_scales[(size_t)b * a.M + mrow[m]];
+    };
+    issue(b0, smem);
+    scales(b0);
+    const uint8_t* const xl = smem + (wm * WM + c) * kStepK;
+    const uint8_t* const wl = smem + (BM + wn * WN + (c >> 2) * (WN / 4) + (c & 3)) * kStepK;
+    for (int b = b0; b < b1; ++b) {
+        const int cur = (b - b0) & 1;
+        // This wave's loads have arrived and its reads of the other buffer are
+        // done; after the barrier that holds for every wave.
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        float s[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) s[m] = sx[m] * sw;
+        if (b + 1 < b1) {
+            issue(b + 1, smem + (cur ^ 1) * kBuf);
+            scales(b + 1);
+        }
+        i32x8_t xf[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xf[m] = operand(xl + cur * kBuf + 16 * m * kStepK, g, key);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const i32x8_t wf = operand(wl + cur * kBuf + 4 * n * kStepK, g, key);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float4_t d = mfma_block(wf, xf[m]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[n][m][q] = __builtin_fmaf(d[q], s[m], acc[n][m][q]);
+            }
+        }
+    }
+    if (a.S > 1) {
+        if (!merge_slices<NT * MT * 4>(a, tm * a.tiles_n + tn, slice, W * 64, true, (float*)acc)) return;
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int row = m0 + wm * WM + 16 * m + c, col = nw + g * (WN / 4);
+        if (row >= a.M) continue;
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {   // 8 columns, whole or absent
+            if (col + 4 * n >= a.N) continue;
+            const float f[8] = {acc[n][m][0],     acc[n][m][1],     acc[n][m][2],     acc[n][m][3],
+                                acc[n + 1][m][0], acc[n + 1][m][1], acc[n + 1][m][2], acc[n + 1][m][3]};
+            store8(a.y, a.y_dtype, (size_t)row * a.N + col + 4 * n, f);
+        }
+    }
+}
+
+// ---- plan ----
+
+typedef void (*kernel_t)(GemmArgs);
+
+struct Plan {
+    kernel_t kernel;
+    const char* name;
+    int bm, bn;        // rows and columns of a tile
+    int threads;
+    size_t lds;
+    int S;
+    int floats;        // partial sums of a tile and slice
+    long long tiles_m, tiles_n;
+    long long blocks;
+    size_t ws;
+};
+
+template <int MT, int XR, int NT, int RD, int W>
+void use_skinny(Plan& p, const char* name) {
+    p.kernel = w8a8_skinny_kernel<MT, XR, NT, RD, W>;
+    p.name = name;
+    p.bm = XR, p.bn = 16 * NT, p.threads = W * 64;
+    p.lds = (size_t)W * RD * (16 * NT + XR) * kStepK + kTableFloats * sizeof(float);
+    p.floats = 16 * MT * 16 * NT;
+}
+
+template <int BM, int BN, int WGM, int WGN>
+void use_tiled(Plan& p, const char* name) {
+    p.kernel = w8a8_tiled_kernel<BM, BN, WGM, WGN>;
+    p.name = name;
+    p.bm = BM, p.bn = BN, p.threads = WGM * WGN * 64;
+    p.lds = 2 * (size_t)(BM + BN) * kStepK;
+    p.floats = BM * BN;
+}
+
+constexpr size_t kMaxPartials = (size_t)64 << 20;
+constexpr int kCounters = (int)(w4h::kWsHead / sizeof(unsigned));
+
+// Slices of K so that tiles * S workgroups fill the GPU, each keeping at
+// least min_units units, within the workspace's counters and kMaxPartials.
+int more_slices(const Plan& p, int kb, int S, long long want, int min_units) {
+    const long long tiles = p.tiles_m * p.tiles_n;
+    while (tiles * S * 2 <= want && kb / (2 * S) >= min_units && 2 * S <= kMaxSplit && tiles <= kCounters &&
+           (size_t)tiles * 2 * S * p.floats * sizeof(float) <= kMaxPartials)
+        S *= 2;
+    return S;
+}
+
+Plan make_plan(int M, int N, int K) {
+    Plan p{};
+    const int kb = (K + kStepK - 1) / kStepK, cus = w4h::cu_count();
+    auto count = [&] {
+        p.tiles_m = (M + p.bm - 1) / p.bm;
+        p.tiles_n = (N + p.bn - 1) / p.bn;
+    };
+    int v = w4h::overrides().w8_variant;
+    if (v < 0) v = M <= 8 ? 0 : M <= 16 ? 1 : M <= 32 ? 2 : M <= 64 ? 3 : M <= 512 ? 10 : 11;
+    bool skinny = v < 10;
+    int S = 1;
+    if (skinny) {
+        switch (v) {
+            case 0: use_skinny<1, 8, 1, 3, 8>(p, "skinny8"); break;
+            case 1: use_skinny<1, 16, 1, 2, 8>(p, "skinny16"); break;
+            case 2: use_skinny<2, 32, 1, 3, 4>(p, "skinny32"); break;
+            default: use_skinny<4, 64, 1, 3, 4>(p, "skinny64"); break;
+        }
+        count();
+        // A slice's products of scales fit the workgroup's table.
+        while (((kb + S - 1) / S) * p.bm > kTableFloats) S *= 2;
+        const long long tiles = p.tiles_m * p.tiles_n;
+        if (S > kMaxSplit || (S > 1 && (tiles > kCounters ||
+                                        (size_t)tiles * S * p.floats * sizeof(float) > kMaxPartials)))
+            skinny = false;
+        else
+            S = more_slices(p, kb, S, 4LL * cus, 8);
+    }
+    if (!skinny) {
+        if (v == 11) use_tiled<256, 256, 4, 2>(p, "tiled256");
+        else use_tiled<128, 128, 2, 2>(p, "tiled128");
+        count();
+        S = more_slices(p, kb, 1, 2LL * cus, 8);
+    }
+    if (w4h::overrides().w8_split > 0) S = w4h::overrides().w8_split;
+    p.S = S;
+    const long long tiles = p.tiles_m * p.tiles_n;
+    p.ws = S > 1 ? w4h::ws_bytes((size_t)tiles * S * p.floats * sizeof(float)) : 0;
+    p.blocks = skinny ? (p.tiles_n * S + 7) / 8 * 8 * p.tiles_m : (tiles * S + 7) / 8 * 8;
+    return p;
+}
+
+// The kernels' dynamic LDS may pass the default limit: said once per process and device.
+void allow_lds() {
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices || done[dev].load(std::memory_order_acquire))
+        return;
+    for (const void* k : {(const void*)w8a8_skinny_kernel<1, 8, 1, 3, 8>, (const void*)w8a8_skinny_kernel<1, 16, 1, 2, 8>,
+                          (const void*)w8a8_skinny_kernel<2, 32, 1, 3, 4>, (const void*)w8a8_skinny_kernel<4, 64, 1, 3, 4>,
+                          (const void*)w8a8_tiled_kernel<128, 128, 2, 2>, (const void*)w8a8_tiled_kernel<256, 256, 4, 2>})
+        (void)hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicLds);
+    done[dev].store(true, std::memory_order_release);
+}
+
+int check_shape(int M, int N, int K) {
+    if (M < 1 || N < 8 || N % 8 || K < 16 || K % 16 || K > (1 << 20)) return W4A16_ERR_SHAPE;
+    return W4A16_OK;
+}
+
+}  // namespace
+
+extern "C" int w8a8_workspace_bytes(int M, int N, int K, size_t* bytes) {
+    if (!bytes) return W4A16_ERR_NULL;
+    if (int rc = check_shape(M, N, K)) return rc;
+    *bytes = make_plan(M, N, K).ws;
+    return W4A16_OK;
+}
+
+extern "C" int w8a8_gemm(const void* x, const float* x_scales, const void* w, const float* w_scales,
+                         void* y, int y_dtype, int M, int N, int K, void* workspace,
+                         size_t workspace_bytes, w4a16_stream_t stream) {
+    if (!x || !x_scales || !w || !w_scales || !y) return W4A16_ERR_NULL;
+    if (y_dtype != W4A16_F16 && y_dtype != W4A16_BF16 && y_dtype != W4A16_F32) return W4A16_ERR_DTYPE;
+    if (int rc = check_shape(M, N, K)) return rc;
+    if (!w4h::aligned16(x) || !w4h::aligned16(x_scales) || !w4h::aligned16(w) ||
+        !w4h::aligned16(w_scales) || !w4h::aligned16(y) || !w4h::aligned16(workspace))
+        return W4A16_ERR_ALIGN;
+    const Plan p = make_plan(M, N, K);
+    if (p.blocks > 0x7fffffffLL) return W4A16_ERR_UNSUPPORTED;
+    if (p.ws && !workspace) return W4A16_ERR_NULL;
+    if (workspace_bytes < p.ws) return W4A16_ERR_WORKSPACE;
+    GemmArgs a{(const uint8_t*)x, x_scales, (const uint8_t*)w, w_scales, y,
+               (float*)w4h::ws_part(workspace), (unsigned*)workspace, y_dtype, M, N, K,
+               (K + kStepK - 1) / kStepK, p.S, (int)p.tiles_n, (int)p.tiles_m};
+    allow_lds();
+    w4h::begin_launches();
+    hipLaunchKernelGGL(p.kernel, dim3((unsigned)p.blocks), dim3(p.threads), p.lds, (hipStream_t)stream, a);
+    w4h::set_last_variant("w8a8_gemm %s tiles=%lldx%lld slices=%d threads=%d lds=%zu", p.name, p.tiles_m,
+                          p.tiles_n, p.S, p.threads, p.lds);
+    return w4h::launch_status();
+}

@@ -1,0 +1,218 @@
+// w8a8_rows.hip -- the row operators of the 8-bit layer: RMS norm with the
+// residual's addition, and the gated product, both with e4m3 output and one
+// fp32 scale for each 128 columns of a row.
+//
+// Both are one pass over memory: every element is loaded once, lives in
+// registers as fp32 until its row's (or block's) statistic is known, and is
+// stored once.  Eight consecutive elements belong to a lane, so the 16 lanes
+// of a DPP row hold exactly one block of 128 columns and its largest
+// magnitude takes four DPP steps, no LDS.
+#include "w8a8_common.h"
+
+using namespace w4k;
+
+namespace {
+
+struct NormArgs {
+    const void* x;
+    const void* residual;
+    const void* weight;
+    void* h;
+    void* y;
+    uint8_t* q;
+    float* scales;
+    long long ldx;
+    int x_dtype, residual_dtype, weight_dtype, y_dtype;
+    int M, K;
+    float eps;
+};
+
+// The sum over a wave, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+// One row per workgroup, P vectors of 8 columns per lane: vector p of lane t
+// is number p * blockDim.x + t, so a wave's loads are contiguous and a block
+// of 128 columns stays inside 16 lanes (blockDim.x is a multiple of 64).
+// K / 8 vectors do not fill the last ones; those lanes load nothing and add
+// zeros.
+template <int P>
+__global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormArgs a) {
+    const int t = threadIdx.x, threads = blockDim.x;
+    const size_t row = blockIdx.x;
+    const int nv = a.K / 8;
+    float h[P][8], w[P][8];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int v = p * threads + t;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[p][e] = w[p][e] = 0.f;
+        if (v < nv) {
+            load8(a.x, a.x_dtype, row * (size_t)a.ldx + 8 * (size_t)v, h[p]);
+            load8(a.weight, a.weight_dtype, 8 * (size_t)v, w[p]);
+        }
+    }
+    if (a.residual) {
+        float r[P][8];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int v = p * threads + t;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[p][e] = 0.f;
+            if (v < nv) load8(a.residual, a.residual_dtype, row * a.K + 8 * (size_t)v, r[p]);
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int v = p * threads + t;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[p][e] += r[p][e];
+            if (a.h && v < nv) store8(a.h, a.residual_dtype, row * a.K + 8 * (size_t)v, h[p]);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[p][e], h[p][e], ss);
+    ss = wave_sum(ss);
+    __shared__ float part[16];
+    if ((t & 63) == 0) part[t >> 6] = ss;
+    __syncthreads();
+    float total = 0.f;
+    for (int i = 0; i < threads >> 6; ++i) total += part[i];
+    const float rstd = 1.0f / __builtin_sqrtf(total / (float)a.K + a.eps);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int v = p * threads + t;
+        float n[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) n[e] = h[p][e] * rstd * w[p][e];
+        if (a.y && v < nv) store8(a.y, a.y_dtype, row * a.K + 8 * (size_t)v, n);
+        if (a.q) {
+            // Lanes past the row's end hold zeros: they leave the maximum as it is.
+            const float s = block_scale(n);
+            if (v < nv) {
+                store_q8(a.q + row * a.K + 8 * (size_t)v, n, s);
+                if ((t & 15) == 0) a.scales[(size_t)(v >> 4) * a.M + row] = s;
+            }
+        }
+    }
+}
+
+// g / (1 + exp(-g)) from the hardware's 2^t and reciprocal (about one ulp
+// each; IEEE division and expf would make the operator bound by the VALU).
+// t = -g log2(e) is taken in two pieces, the rounding of the product and the
+// rest of the constant, so that 2^t keeps its relative error for large |g|.
+// exp(-g) past fp32's range is infinite and the result 0, as in the formula.
+__device__ __forceinline__ float silu(float g) {
+    constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+    const float t = -g * kLog2e;
+    const float rest = __builtin_fmaf(-g, kLog2eRest, __builtin_fmaf(-g, kLog2e, -t));
+    float p = __builtin_amdgcn_exp2f(t);
+    // Not where p is 0 or infinite: there the correction could be 0 * inf.
+    const float c = p * (kLn2 * rest);
+    p = __builtin_fabsf(t) < 126.0f ? p + c : p;
+    return g * __builtin_amdgcn_rcpf(1.0f + p);
+}
+
+struct GatedArgs {
+    const void* x;
+    void* y;
+    uint8_t* q;
+    float* scales;
+    long long ldx;
+    int x_dtype, y_dtype;
+    int M, K;
+    int chunks;   // workgroups per row
+};
+
+constexpr int kGatedThreads = 256;
+constexpr int kGatedCols = kGatedThreads * 8;
+
+// A workgroup takes 2048 columns of one row; a block of 128 columns is 16 lanes.
+__global__ __launch_bounds__(kGatedThreads) void silu_mul_quant_kernel(GatedArgs a) {
+    const size_t row = blockIdx.x / (unsigned)a.chunks;
+    const int chunk = blockIdx.x % (unsigned)a.chunks;
+    const int k = chunk * kGatedCols + (int)threadIdx.x * 8;
+    float g[8], u[8], n[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.f;
+    if (k < a.K) {
+        load8(a.x, a.x_dtype, row * (size_t)a.ldx + k, g);
+        load8(a.x, a.x_dtype, row * (size_t)a.ldx + a.K + k, u);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) n[e] = silu(g[e]) * u[e];
+    if (a.y && k < a.K) store8(a.y, a.y_dtype, row * a.K + k, n);
+    if (a.q) {
+        const float s = block_scale(n);
+        if (k < a.K) {
+            store_q8(a.q + row * a.K + k, n, s);
+            if ((threadIdx.x & 15) == 0) a.scales[(size_t)(k >> 7) * a.M + row] = s;
+        }
+    }
+}
+
+bool dtype_ok(int d) { return d == W4A16_F16 || d == W4A16_BF16 || d == W4A16_F32; }
+
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxNormPasses = 4;
+constexpr int kMaxNormK = kMaxThreads * 8 * kMaxNormPasses;
+
+// Output checks shared by the row operators: y, or q with its scales, or all.
+int check_out(const void* y, int y_dtype, const void* q, const float* scales) {
+    if (!y && !q) return W4A16_ERR_NULL;
+    if (!q != !scales) return W4A16_ERR_NULL;
+    if (y && !dtype_ok(y_dtype)) return W4A16_ERR_DTYPE;
+    if (!w4h::aligned16(y) || !w4h::aligned16(q) || !w4h::aligned16(scales)) return W4A16_ERR_ALIGN;
+    return W4A16_OK;
+}
+
+}  // namespace
+
+extern "C" int w8a8_rmsnorm_quant(const void* x, int x_dtype, long long ldx, const void* residual,
+                                  int residual_dtype, void* h_out, const void* weight,
+                                  int weight_dtype, float eps, void* y_out, int y_dtype, void* q,
+                                  float* scales, int M, int K, w4a16_stream_t stream) {
+    if (!x || !weight || (h_out && !residual)) return W4A16_ERR_NULL;
+    if (!dtype_ok(x_dtype) || !dtype_ok(weight_dtype) || (residual && !dtype_ok(residual_dtype)))
+        return W4A16_ERR_DTYPE;
+    if (M < 1 || K < 16 || K % 16 || ldx < K || ldx % 8 || !(eps >= 0.f) || eps > 3.4e38f)
+        return W4A16_ERR_SHAPE;
+    if (!w4h::aligned16(x) || !w4h::aligned16(residual) || !w4h::aligned16(h_out) ||
+        !w4h::aligned16(weight))
+        return W4A16_ERR_ALIGN;
+    if (int rc = check_out(y_out, y_dtype, q, scales)) return rc;
+    if (K > kMaxNormK) return W4A16_ERR_UNSUPPORTED;
+    NormArgs a{x, residual, weight, h_out, y_out, (uint8_t*)q, scales, ldx, x_dtype,
+               residual_dtype, weight_dtype, y_dtype, M, K, eps};
+    const int nv = K / 8;
+    const int P = nv <= kMaxThreads ? 1 : nv <= 2 * kMaxThreads ? 2 : 4;
+    const int threads = (((nv + P - 1) / P) + 63) / 64 * 64;
+    w4h::begin_launches();
+    auto kernel = P == 1 ? rmsnorm_quant_kernel<1> : P == 2 ? rmsnorm_quant_kernel<2> : rmsnorm_quant_kernel<4>;
+    hipLaunchKernelGGL(kernel, dim3(M), dim3(threads), 0, (hipStream_t)stream, a);
+    w4h::set_last_variant("w8a8_rmsnorm passes=%d threads=%d rows=%d", P, threads, M);
+    return w4h::launch_status();
+}
+
+extern "C" int w8a8_silu_mul_quant(const void* x, int x_dtype, long long ldx, void* y_out,
+                                   int y_dtype, void* q, float* scales, int M, int K,
+                                   w4a16_stream_t stream) {
+    if (!x) return W4A16_ERR_NULL;
+    if (!dtype_ok(x_dtype)) return W4A16_ERR_DTYPE;
+    if (M < 1 || K < 16 || K % 16 || K > (1 << 30) || ldx < 2LL * K || ldx % 8) return W4A16_ERR_SHAPE;
+    if (!w4h::aligned16(x)) return W4A16_ERR_ALIGN;
+    if (int rc = check_out(y_out, y_dtype, q, scales)) return rc;
+    const long long chunks = (K + kGatedCols - 1) / kGatedCols;
+    if (chunks * M > 0x7fffffffLL) return W4A16_ERR_SHAPE;
+    GatedArgs a{x, y_out, (uint8_t*)q, scales, ldx, x_dtype, y_dtype, M, K, (int)chunks};
+    w4h::begin_launches();
+    hipLaunchKernelGGL(silu_mul_quant_kernel, dim3((unsigned)(chunks * M)), dim3(kGatedThreads), 0,
+                       (hipStream_t)stream, a);
+    w4h::set_last_variant("w8a8_silu_mul chunks=%lld rows=%d", chunks, M);
+    return w4h::launch_status();
+}
