@@ -132,7 +132,7 @@ template <int MT, int XR, int NT, int RD, int W>
 __global__ __launch_bounds__(W * 64) void w8a8_skinny_kernel(GemmArgs a) {
     constexpr int kSlot = (16 * NT + XR) * kStepK;
     constexpr int kLoads = 2 * NT + XR / 8;
-    extern __shared__ uint8_t smem[];
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     float* const table = (float*)(smem + W * RD * kSlot);   // [unit of the slice][XR]
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
 
@@ -278,7 +278,7 @@ __global__ __launch_bounds__(WGM * WGN * 64) void w8a8_tiled_kernel(GemmArgs a) 
     constexpr int kBuf = (BM + BN) * kStepK;
     constexpr int XL = BM / (8 * W), WL = BN / (8 * W);   // loads per wave and step
     static_assert(XL >= 1 && WL >= 1 && WN <= 128 && WN >= 32, "tile shape");
-    extern __shared__ uint8_t smem[];
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
     const int wm = wave % WGM, wn = wave / WGM;
 
