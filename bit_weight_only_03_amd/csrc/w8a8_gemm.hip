@@ -32,8 +32,9 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every descriptor here: reads zeros
 constexpr int kStepK = 128;                  // k per step: one scale block, one MFMA
 constexpr int kMaxSplit = 64;
-constexpr int kMaxDynamicLds = 159 * 1024;   // a CU's 160 KiB less the kernels' static variables
+constexpr int kMaxDynamicLds = 160 * 1024;
 constexpr int kMaxDevices = 64;
+constexpr int kMaxM = 1 << 26;               // a block's x_scales in one 32-bit descriptor
 
 struct GemmArgs {
     const uint8_t* x;
@@ -87,7 +88,7 @@ __device__ __forceinline__ void store4(const GemmArgs& a, int m, int n, const fl
 // f then holds the sums.  No workgroup waits for another.
 template <int C>
 __device__ __forceinline__ bool merge_slices(const GemmArgs& a, int tile, int slice, int threads, bool live,
-                                             float* f) {
+                                             unsigned* arrived, float* f) {
     const int t = threadIdx.x;
     float* const base = a.part + (size_t)tile * a.S * C * threads;
     if (live) {
@@ -97,11 +98,10 @@ __device__ __forceinline__ bool merge_slices(const GemmArgs& a, int tile, int sl
                                __HIP_MEMORY_SCOPE_AGENT);
     }
     __builtin_amdgcn_s_waitcnt(0);   // this thread's stores are done
-    __shared__ unsigned arrived;
     __syncthreads();
-    if (t == 0) arrived = __hip_atomic_fetch_add(a.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (t == 0) *arrived = __hip_atomic_fetch_add(a.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
-    if (arrived != (unsigned)(a.S - 1)) return false;
+    if (*arrived != (unsigned)(a.S - 1)) return false;
     if (t == 0) __hip_atomic_store(a.counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (live) {
         float v[C];
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(W * 64) void w8a8_skinny_kernel(GemmArgs a) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) f[q] += red[((wv * kTiles + wave) * 4 + q) * 64 + lane];
     }
-    if (a.S > 1 && !merge_slices<4>(a, tile * a.tiles_m + mb, slice, kTiles * 64, live, f)) return;
+    if (a.S > 1 && !merge_slices<4>(a, tile * a.tiles_m + mb, slice, kTiles * 64, live, (unsigned*)table, f)) return;
     if (live) store4(a, m, n, f);
 }
 
@@ -275,8 +275,10 @@ __global__ __launch_bounds__(W * 64) void w8a8_skinny_kernel(GemmArgs a) {
 template <int BM, int BN, int WGM, int WGN>
 __global__ __launch_bounds__(WGM * WGN * 64) void w8a8_tiled_kernel(GemmArgs a) {
     constexpr int W = WGM * WGN, WM = BM / WGM, WN = BN / WGN, MT = WM / 16, NT = WN / 16;
-    constexpr int kBuf = (BM + BN) * kStepK;
+    constexpr int kXBuf = BM * kStepK, kWBuf = BN * kStepK;
     constexpr int XL = BM / (8 * W), WL = BN / (8 * W);   // loads per wave and step
+    constexpr int kAll = XL + WL;
+    constexpr int kLag = 3;   // products under way between one and its scaling (1: 691, 2: 678, 3: 665, 4: 672 us)
     static_assert(XL >= 1 && WL >= 1 && WN <= 128 && WN >= 32, "tile shape");
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
@@ -312,22 +314,20 @@ __global__ __launch_bounds__(WGM * WGN * 64) void w8a8_tiled_kernel(GemmArgs a) 
 #pragma unroll
     for (int j = 0; j < WL; ++j) woff[j] = (uint32_t)(8 * (j * W + wave) + row8) * K + 16u * wchunk;
 
-    auto issue = [&](int b, uint8_t* buf) {
-        const uint32_t k = (uint32_t)b * kStepK;
-        const bool xout = b == last && 16 * xchunk >= tail, wout = b == last && 16 * wchunk >= tail;
-#pragma unroll
-        for (int j = 0; j < XL; ++j) load_lds(rx, buf + (j * W + wave) * 1024, xout ? kOutside : xoff[j], k);
-#pragma unroll
-        for (int j = 0; j < WL; ++j)
-            load_lds(rw, buf + BM * kStepK + (j * W + wave) * 1024, wout ? kOutside : woff[j], k);
+    // Load j of this wave: of block b of x into ring slot i (of 2), of w into slot i (of 3).
+    auto issue_x = [&](int j, int b, int i) {
+        load_lds(rx, smem + i * kXBuf + (j * W + wave) * 1024, b == last && 16 * xchunk >= tail ? kOutside : xoff[j],
+                 (uint32_t)b * kStepK);
+    };
+    auto issue_w = [&](int j, int b, int i) {
+        load_lds(rw, smem + 2 * kXBuf + i * kWBuf + (j * W + wave) * 1024,
+                 b == last && 16 * wchunk >= tail ? kOutside : woff[j], (uint32_t)b * kStepK);
     };
 
     const int c = lane & 15, g = lane >> 4, key = c & 7;
     const int nw = n0 + wn * WN;   // this wave's first column; all of them in one scale block
     const float* const ws = a.w_scales + (size_t)(min(nw, a.N - 1) >> 7) * a.kb;
-    int mrow[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) mrow[m] = min(m0 + wm * WM + 16 * m + c, a.M - 1);
+    const uint32_t xs_off = (uint32_t)(m0 + wm * WM + c) * 4u;   // rows past M read scales of 0
     float4_t acc[NT][MT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -335,45 +335,86 @@ __global__ __launch_bounds__(WGM * WGN * 64) void w8a8_tiled_kernel(GemmArgs a) 
         for (int m = 0; m < MT; ++m) acc[n][m] = float4_t{0.f, 0.f, 0.f, 0.f};
 
     float sx[MT], sw;
+    const __amdgpu_buffer_rsrc_t rws = make_rsrc(ws, (uint32_t)a.kb * 4u);
     auto scales = [&](int b) {
-        sw = ws[b];
+        const __amdgpu_buffer_rsrc_t rxs = make_rsrc(a.x_scales + (size_t)b * a.M, (uint32_t)a.M * 4u);
+        sw = bitcast<float>(__builtin_amdgcn_raw_buffer_load_b32(rws, 0, (uint32_t)b * 4u, 0));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) sx[m] = a.x_scales[(size_t)b * a.M + mrow[m]];
+        for (int m = 0; m < MT; ++m)
+            sx[m] = bitcast<float>(__builtin_amdgcn_raw_buffer_load_b32(rxs, xs_off + 64u * m, 0, 0));
     };
-    issue(b0, smem);
     scales(b0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < XL; ++j) issue_x(j, b0, 0);
+#pragma unroll
+    for (int j = 0; j < WL; ++j) issue_w(j, b0, 0);
+#pragma unroll
+    for (int j = 0; j < WL; ++j) issue_w(j, min(b0 + 1, b1 - 1), 1);
+    __builtin_amdgcn_sched_barrier(0);
+    float s[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) s[m] = sx[m] * sw;
     const uint8_t* const xl = smem + (wm * WM + c) * kStepK;
-    const uint8_t* const wl = smem + (BM + wn * WN + (c >> 2) * (WN / 4) + (c & 3)) * kStepK;
+    const uint8_t* const wl = smem + 2 * kXBuf + (wn * WN + (c >> 2) * (WN / 4) + (c & 3)) * kStepK;
+    int xs = 0, ws3 = 0;
     for (int b = b0; b < b1; ++b) {
-        const int cur = (b - b0) & 1;
-        // This wave's loads have arrived and its reads of the other buffer are
-        // done; after the barrier that holds for every wave.
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        // This wave's loads of this block have arrived (those of the next
+        // block of w may still be on their way) and its reads of the last
+        // block are done; after the barrier that holds for every wave.
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(WL) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        float s[MT];
+        const uint8_t* const xb = xl + xs * kXBuf;
+        const uint8_t* const wb = wl + ws3 * kWBuf;
+        xs ^= 1;
+        const int fill = ws3 == 0 ? 2 : ws3 - 1;
+        ws3 = ws3 == 2 ? 0 : ws3 + 1;
+        i32x8_t xf[MT], wf[2];
+        wf[0] = operand(wb, g, key);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xf[m] = operand(xb + 16 * m * kStepK, g, key);
+        // The next step's loads; the last step repeats its own, which nothing reads.
+        const int next = min(b + 1, b1 - 1), next2 = min(b + 2, b1 - 1);
+        scales(next);
+        __builtin_amdgcn_sched_barrier(0);
+        // The block sums of kLag products are under way while an older one is scaled and added.
+        float4_t d[kLag + 1];
+#pragma unroll
+        for (int j = 0; j < NT * MT + kLag; ++j) {
+            const int n = j / MT, m = j % MT;
+            if (j < NT * MT) {
+                if (m == 0) {
+                    if (n + 1 < NT) wf[(n + 1) & 1] = operand(wb + 4 * (n + 1) * kStepK, g, key);
+                    // The next loads, over the first three quarters of the step.
+                    const int lo = min(kAll, (n * kAll * 4 + 3 * NT - 1) / (3 * NT));
+                    const int hi = min(kAll, ((n + 1) * kAll * 4 + 3 * NT - 1) / (3 * NT));
+#pragma unroll
+                    for (int i = 0; i < kAll; ++i) {
+                        if (i < lo || i >= hi) continue;
+                        if (i < XL) issue_x(i, next, xs);
+                        else issue_w(i - XL, next2, fill);
+                    }
+                }
+                d[j % (kLag + 1)] = mfma_block(wf[n & 1], xf[m]);
+            }
+            if (j >= kLag) {
+                const int jj = j - kLag, nn = jj / MT, mm = jj % MT;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[nn][mm][q] = __builtin_fmaf(d[jj % (kLag + 1)][q], s[mm], acc[nn][mm][q]);
+            }
+            __builtin_amdgcn_sched_barrier(0);   // products and sums stay in this order
+        }
+        // The next step's scales, from loads older than its operands'.
 #pragma unroll
         for (int m = 0; m < MT; ++m) s[m] = sx[m] * sw;
-        if (b + 1 < b1) {
-            issue(b + 1, smem + (cur ^ 1) * kBuf);
-            scales(b + 1);
-        }
-        i32x8_t xf[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) xf[m] = operand(xl + cur * kBuf + 16 * m * kStepK, g, key);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const i32x8_t wf = operand(wl + cur * kBuf + 4 * n * kStepK, g, key);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const float4_t d = mfma_block(wf, xf[m]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[n][m][q] = __builtin_fmaf(d[q], s[m], acc[n][m][q]);
-            }
-        }
     }
+    // The last loads, which nothing reads, are done before LDS is reused or released.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
     if (a.S > 1) {
-        if (!merge_slices<NT * MT * 4>(a, tm * a.tiles_n + tn, slice, W * 64, true, (float*)acc)) return;
+        if (!merge_slices<NT * MT * 4>(a, tm * a.tiles_n + tn, slice, W * 64, true, (unsigned*)smem, (float*)acc)) return;
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -420,7 +461,7 @@ void use_tiled(Plan& p, const char* name) {
     p.kernel = w8a8_tiled_kernel<BM, BN, WGM, WGN>;
     p.name = name;
     p.bm = BM, p.bn = BN, p.threads = WGM * WGN * 64;
-    p.lds = 2 * (size_t)(BM + BN) * kStepK;
+    p.lds = (size_t)(2 * BM + 3 * BN) * kStepK;
     p.floats = BM * BN;
 }
 
@@ -493,7 +534,7 @@ void allow_lds() {
 }
 
 int check_shape(int M, int N, int K) {
-    if (M < 1 || N < 8 || N % 8 || K < 16 || K % 16 || K > (1 << 20)) return W4A16_ERR_SHAPE;
+    if (M < 1 || M > kMaxM || N < 8 || N % 8 || K < 16 || K % 16 || K > (1 << 20)) return W4A16_ERR_SHAPE;
     return W4A16_OK;
 }
 

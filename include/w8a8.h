@@ -60,7 +60,7 @@ int w8a8_silu_mul_quant(const void* x, int x_dtype, long long ldx, void* y_out, 
  * sums of those in fp32.  Sums over blocks are fp32, the scales' product is
  * formed in fp32 once per row and block; the result is deterministic.
  * y [M][N] contiguous, y_dtype f32, f16 or bf16 (rounded once).  Shape:
- * M >= 1, N >= 8, N % 8 == 0, 16 <= K <= 2^20, K % 16 == 0.  M is not limited to a
+ * 1 <= M <= 2^26, N >= 8, N % 8 == 0, 16 <= K <= 2^20, K % 16 == 0.  M is not limited to a
  * few rows: one token to whole prompts.  x, w, y and the workspace do not overlap.
  * workspace may be NULL where w8a8_workspace_bytes reports 0. */
 int w8a8_workspace_bytes(int M, int N, int K, size_t* bytes);

@@ -85,7 +85,7 @@ def test_gemm_refusals_and_sizes():
         assert gemm(**{p: 0}) == -1
         assert gemm(**{p: GOOD + 8}) == -3
     assert gemm(yd=4) == -4
-    for M, N, K in ((0, 64, 256), (1, 0, 256), (1, 12, 256), (1, 64, 0), (1, 64, 200), (1, 64, (1 << 20) + 16)):
+    for M, N, K in ((0, 64, 256), (1, 0, 256), (1, 12, 256), (1, 64, 0), (1, 64, 200), (1, 64, (1 << 20) + 16), ((1 << 26) + 1, 64, 256)):
         assert gemm(M=M, N=N, K=K) == -2
         assert status(lib.w8a8_workspace_bytes, M, N, K) == -2
     # A long sum over few columns is split: the size query says so, and less is refused.
