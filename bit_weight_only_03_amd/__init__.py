@@ -1,5 +1,6 @@
 """Thin Python binding of libw4a16.so, the gfx950 W4A16 / ternary small-M
-linear-layer library (C ABI declared in include/w4a16.h).
+linear-layer library (C ABI declared in include/w4a16.h, the 8-bit layer's in
+include/w8a8.h, the draft-tree attention's in include/tree_attn.h).
 
 Every function here has the same name and argument order as its C entry
 point and only marshals arguments: tensors (anything with ``data_ptr()``) or
@@ -72,6 +73,11 @@ _SIGS_W8A8 = {
     "w8a8_workspace_bytes": [_I, _I, _I, _PSZ],
     "w8a8_gemm": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _SZ, _P],
 }
+_SIGS_TREE = {
+    "tree_attn_workspace_bytes": [_I, _I, _I, _I, _I, _I, _PSZ],
+    "tree_attn": [_P, _L, _P, _P, _I, _I, _I, _L, _L, _L, _P, _I, _P, _I, _P, _F, _P, _P, _I, _I, _I,
+                  _I, _I, _P, _SZ, _P],
+}
 _STR_RESULT = ("w4a16_status_string", "w4a16_last_variant", "w4a16_last_error")
 
 _lib_handle = None
@@ -86,7 +92,7 @@ def _lib_get():
             raise ImportError(f"{LIB_PATH} is missing: build it with "
                               "`python -m bit_weight_only_03_amd.build`")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, args in (*_SIGS.items(), *_SIGS_W8A8.items()):
+        for name, args in (*_SIGS.items(), *_SIGS_W8A8.items(), *_SIGS_TREE.items()):
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = ctypes.c_char_p if name in _STR_RESULT else _I
@@ -103,6 +109,7 @@ _lib = _LazyLib()
 
 EXPORTED = tuple(_SIGS)
 EXPORTED_W8A8 = tuple(_SIGS_W8A8)
+EXPORTED_TREE = tuple(_SIGS_TREE)
 
 
 def _ptr(t):
@@ -339,3 +346,20 @@ def w8a8_gemm(x, x_scales, w, w_scales, y, y_dtype, M, N, K, workspace=None, wor
     _check("w8a8_gemm", _lib.w8a8_gemm(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(y),
                                        _dt(y_dtype), M, N, K, _ptr(workspace), workspace_bytes,
                                        _stream(stream)))
+
+
+def tree_attn_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    b = _SZ()
+    _check("tree_attn_workspace_bytes",
+           _lib.tree_attn_workspace_bytes(B, T, Hq, Hkv, D, max_len, ctypes.byref(b)))
+    return b.value
+
+
+def tree_attn(q, q_stride, k, v, dtype, num_pages, page_size, page_stride, token_stride, head_stride,
+              block_table, table_stride, lens, max_len, tree_mask, scale, out, lse, B, T, Hq, Hkv, D,
+              workspace=None, workspace_bytes=0, stream=None):
+    _check("tree_attn", _lib.tree_attn(
+        _ptr(q), q_stride, _ptr(k), _ptr(v), _dt(dtype), num_pages, page_size, page_stride,
+        token_stride, head_stride, _ptr(block_table), table_stride, _ptr(lens), max_len,
+        _ptr(tree_mask), scale, _ptr(out), _ptr(lse), B, T, Hq, Hkv, D, _ptr(workspace),
+        workspace_bytes, _stream(stream)))
