@@ -16,10 +16,13 @@
 // column (D/16) r + t: it loads D/16 consecutive columns of each key and pairs
 // them up with one byte permute per register.
 //
-// Tiles of K and V go from the cache straight to LDS, whole rows of a page, two
+// Tiles of K and V go from the cache straight to LDS, whole rows of a page, NS
 // tiles deep per group.  K's 16-byte chunks are permuted with the key on the
 // way, so that reading one chunk of 16 keys is free of bank conflicts.
+#include <math.h>
+
 #include <atomic>
+#include <type_traits>
 
 #include "w8a8_common.h"
 #include "../../include/tree_attn.h"
@@ -52,10 +55,22 @@ struct TreeArgs {
     long long q_stride, page_stride, token_stride, head_stride;
     int num_pages, page_shift, table_stride;
     int max_len;
-    float scale2;      // scale * log2(e)
+    float scale2;      // |scale| log2(e)
+    uint32_t q_sign;   // the sign bits of two elements of q where scale is negative
     int B, T, Hq, Hkv, G, R;
     int S, RB;         // splits of the keys, blocks of rows
 };
+
+// Waits until at most N of this wave's loads are under way and its LDS reads
+// are done.  The builtin and not an asm statement: the compiler then knows what
+// has arrived, and does not wait for the youngest loads by itself.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "six bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (0 << 8) | ((N >> 4) << 14));
+    asm volatile("" ::: "memory");
+}
 
 template <bool BF16>
 __device__ __forceinline__ float4_t mfma(const u32x4_t& a, const u32x4_t& b, const float4_t& c) {
@@ -79,6 +94,13 @@ template <bool BF16>
 __device__ __forceinline__ bool not_finite(uint32_t h) {
     constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
     return (h & kExp) == kExp;
+}
+
+// Which of a tile's 32 keys a row sees, the first of them draft d0 (negative:
+// that many keys of context come first).  see: the row's mask, no bit past T.
+__device__ __forceinline__ uint32_t visible(uint64_t see, int d0) {
+    if (d0 >= 0) return d0 < 64 ? (uint32_t)(see >> d0) : 0u;
+    return d0 <= -32 ? ~0u : (uint32_t)(see << -d0) | ((1u << -d0) - 1u);
 }
 
 // The largest (sum) over the four lanes that hold one row, 16 apart.
@@ -113,8 +135,8 @@ __device__ __forceinline__ size_t out_row(const TreeArgs& a, int b, int kvh, int
     return ((size_t)b * a.T + row / a.G) * a.Hq + kvh * a.G + row % a.G;
 }
 
-template <bool BF16, int D, int RT, int WK, int WR>
-__global__ __launch_bounds__(WK* WR * 64) void tree_attn_kernel(TreeArgs a) {
+template <bool BF16, int D, int RT, int WK, int WR, int NS>
+__global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
     constexpr int DT = D / 16;                 // operand tiles of O^T
     constexpr int KS = D / 32;                 // products per score tile
     constexpr int kChunks = D / 8;             // 16-byte chunks of a key
@@ -141,31 +163,68 @@ __global__ __launch_bounds__(WK* WR * 64) void tree_attn_kernel(TreeArgs a) {
     const int nt = t1 - t0 > kg ? (t1 - t0 - kg + WK - 1) / WK : 0;   // this group's tiles
     const int loops = (t1 - t0 + WK - 1) / WK;                        // the same for every group (barriers)
 
-    const int* const table = a.table + (size_t)b * a.table_stride;
+    // The page of position p, by a scalar load (the table does not change while the kernel runs).
+    typedef const __attribute__((address_space(4))) int* const_ptr_t;
+    const const_ptr_t table = (const_ptr_t)(a.table + (size_t)b * a.table_stride);
+    auto page_of = [&](int p) {
+        return min(max(table[min(p, total - 1) >> a.page_shift], 0), a.num_pages - 1);
+    };
     const long long head = kvh * a.head_stride;
-    uint8_t* const ring = smem + kg * 2 * kStage;
+    uint8_t* const ring = smem + kg * NS * kStage;
+    constexpr int VW = D / 32;   // dwords of a key of V per lane
+    constexpr int VH = VW < 4 ? VW : 4;
     const int key_in = lane / kChunks, pos = lane % kChunks;
 
-    // Lane j of 32: the page of key j of the group's tile n (the last key's
-    // page past the end).
-    auto page_of = [&](int n) {
-        const int p = min((t0 + kg + n * WK) * kTile + (lane & 31), total - 1);
-        return min(max(table[p >> a.page_shift], 0), a.num_pages - 1);
+    // A load instruction takes whole keys of one page: its base is scalar, its
+    // lane offsets constant.  (Buffer loads and not global ones: the compiler
+    // waits for every global load into LDS before any LDS read.)  A wave loads
+    // kSpan keys of a tile, which lie in one page, or in two halves of a page
+    // each, or (short pages) are taken page by page with the other lanes off.
+    constexpr int kSpan = kPer * kKeys;
+    const uint32_t key_bytes = (uint32_t)(a.token_stride * 2);
+    const uint32_t page_bytes = (uint32_t)((1u << a.page_shift) - 1) * key_bytes + D * 2;
+    const int page_mask = (1 << a.page_shift) - 1;
+    const uint32_t k_lane = 16u * (pos ^ key_in), v_lane = 16u * pos, row_lane = key_in * key_bytes;
+    const bool counted = page_mask >= kKeys - 1;   // a tile then takes 2 kPer loads of a wave
+    const int runs = page_mask >= kSpan - 1 ? 1 : kPer > 1 && page_mask >= kSpan / 2 - 1 ? 2 : 0;
+    auto first_of = [&](int n) { return (t0 + kg + n * WK) * kTile; };   // the group's tile n
+    auto load = [&](uint8_t* to, int i, const __amdgpu_buffer_rsrc_t& rk, const __amdgpu_buffer_rsrc_t& rv,
+                    uint32_t row, uint32_t in_page) {
+        const uint32_t k_off = k_lane ^ (16u * ((i * kKeys) & kSwz));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr_t)(to + i * 1024), 16, row + k_off, in_page, 0, kAux);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr_t)(to + kHalf + i * 1024), 16, row + v_lane, in_page, 0, kAux);
     };
-    auto issue = [&](int n, int pages) {
-        uint8_t* const to = ring + (n & 1) * kStage;
-        const int first = (t0 + kg + n * WK) * kTile;
+    auto of_k = [&](int page) { return make_rsrc(a.k + ((long long)page * a.page_stride + head), page_bytes); };
+    auto of_v = [&](int page) { return make_rsrc(a.v + ((long long)page * a.page_stride + head), page_bytes); };
+    int pages[2];   // of the two halves of the tile that is issued next
+    auto look_up = [&](int n) {
+        const int p = first_of(n) + wr * kSpan;
+        pages[0] = pages[1] = page_of(p);
+        if (runs == 2) pages[1] = page_of(p + kSpan / 2);
+    };
+    // Tile n (past the last one, the last one again: nothing reads it) into ring slot n.
+    auto issue = [&](int n) {
+        uint8_t* const to = ring + (n % NS) * kStage;
+        const int first = first_of(min(n, nt - 1)) + wr * kSpan;
+        if (runs) {
+            uint32_t in_page = (uint32_t)(first & page_mask) * key_bytes;
+            __amdgpu_buffer_rsrc_t rk = of_k(pages[0]), rv = of_v(pages[0]);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int j = (wr * kPer + i) * kKeys + key_in;      // key of the tile
-            const int p = min(first + j, total - 1);
-            const long long row = (long long)__shfl(pages, j) * a.page_stride +
-                                  (long long)(p & ((1 << a.page_shift) - 1)) * a.token_stride + head;
-            const uint16_t* const kp = a.k + row + 8 * (pos ^ (j & kSwz));
-            const uint16_t* const vp = a.v + row + 8 * pos;
-            uint8_t* const at = to + (wr * kPer + i) * 1024;
-            __builtin_amdgcn_global_load_lds((global_ptr_t)kp, (lds_ptr_t)at, 16, 0, kAux);
-            __builtin_amdgcn_global_load_lds((global_ptr_t)vp, (lds_ptr_t)(at + kHalf), 16, 0, kAux);
+            for (int i = 0; i < kPer; ++i) {
+                if (i == kPer / 2 && runs == 2) rk = of_k(pages[1]), rv = of_v(pages[1]), in_page = 0;
+                load(to, wr * kPer + i, rk, rv, row_lane, in_page);
+                in_page += kKeys * key_bytes;
+            }
+            look_up(min(n + 1, nt - 1));
+        } else {
+            const int step = counted ? kKeys : page_mask + 1;
+#pragma unroll 1
+            for (int j = 0; j < kSpan; j += step) {
+                const int page = page_of(first + j);
+                const uint32_t in_page = (uint32_t)((first + j) & page_mask) * key_bytes;
+                if (counted || (key_in & ~page_mask) == (j & (kKeys - 1)))
+                    load(to, wr * kPer + j / kKeys, of_k(page), of_v(page), counted ? row_lane : (key_in & page_mask) * key_bytes, in_page);
+            }
         }
     };
 
@@ -178,11 +237,12 @@ __global__ __launch_bounds__(WK* WR * 64) void tree_attn_kernel(TreeArgs a) {
         const int row = row0 + 16 * rt + c;
         const bool there = row < a.R;
         const int tok = there ? row / a.G : 0;
-        see[rt] = there ? a.mask[(size_t)b * a.T + tok] : 0;
+        see[rt] = there ? a.mask[(size_t)b * a.T + tok] & (~0ull >> (64 - a.T)) : 0;
         const uint16_t* const qp = a.q + ((size_t)b * a.T + tok) * a.q_stride + (size_t)(kvh * a.G + (there ? row % a.G : 0)) * D;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) qf[rt][s] = there ? *(const u32x4_t*)(qp + 32 * s + 8 * g) : u32x4_t{0, 0, 0, 0};
+        for (int s = 0; s < KS; ++s) qf[rt][s] = there ? *(const u32x4_t*)(qp + 32 * s + 8 * g) ^ a.q_sign : u32x4_t{0, 0, 0, 0};
     }
+    bool any_odd = false;   // the same for the whole wave
     float4_t o[RT][DT];
     float m[RT], l[RT];
 #pragma unroll
@@ -192,51 +252,10 @@ __global__ __launch_bounds__(WK* WR * 64) void tree_attn_kernel(TreeArgs a) {
         for (int d = 0; d < DT; ++d) o[rt][d] = float4_t{0.f, 0.f, 0.f, 0.f};
     }
 
-    int pages = 0;   // of the tile that is issued next
-    if (nt > 0) {
-        const int pages0 = page_of(0);
-        pages = page_of(min(1, nt - 1));
-        issue(0, pages0);
-    }
-    for (int n = 0; n < loops; ++n) {
-        const bool live = n < nt;
-        if constexpr (WR == 1) {
-            if (!live) break;
-        }
-        // The next tile's loads go out before this one is waited for (one wave
-        // to a group: the other buffer is its own and read), or after the
-        // barrier that says the other buffer is read.  The page numbers of the
-        // tile after it are asked for before them, so that waiting for the
-        // numbers never waits for these loads.  Past the last tile the last one
-        // is loaded again, which nothing reads.
-        const int after = min(n + 1, nt - 1);
-        if constexpr (WR == 1) {
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            const int next = page_of(min(n + 2, nt - 1));
-            __builtin_amdgcn_sched_barrier(0);
-            if (after > n) issue(after, pages);
-            __builtin_amdgcn_sched_barrier(0);
-            pages = next;
-            if (after > n)
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kPer) : "memory");
-            else
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        } else {
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            if (live && after > n) {
-                const int next = page_of(min(n + 2, nt - 1));
-                issue(after, pages);
-                pages = next;
-            }
-            if (!live) continue;
-        }
-        const uint8_t* const kt = ring + (n & 1) * kStage;
-        const uint8_t* const vt = kt + kHalf;
-        const int first = (t0 + kg + n * WK) * kTile;
-        const bool edge = first + kTile > len;   // drafts or the end inside (the same for the whole wave)
-
+    // One tile: scores, probabilities, product with V.  EDGE: some of its keys
+    // are drafts or past the end.
+    auto tile = [&](auto edge, const uint8_t* kt, const uint8_t* vt, int first) {
+        constexpr bool EDGE = decltype(edge)::value;
         float4_t sc[2][RT];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -250,24 +269,22 @@ __global__ __launch_bounds__(WK* WR * 64) void tree_attn_kernel(TreeArgs a) {
             }
         }
         u32x4_t pf[RT];   // probabilities: the B operand of the product with V
+        const int d0 = first - len;   // the tile's first key among the drafts (negative: context)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][rt][i & 3] * a.scale2;
-            if (edge) {
+            for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][rt][i & 3];
+            if constexpr (EDGE) {
+                const uint32_t bits = visible(see[rt], d0) >> (4 * g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int p = first + 16 * (i >> 2) + 4 * g + (i & 3), j = p - len;
-                    const bool sees = j < 0 || (j < a.T && ((see[rt] >> (j & 63)) & 1));
-                    x[i] = sees ? x[i] : -__builtin_inff();
-                }
+                for (int i = 0; i < 8; ++i)
+                    x[i] = (bits >> (16 * (i >> 2) + (i & 3))) & 1u ? x[i] : -__builtin_inff();
             }
             float top = x[0];
 #pragma unroll
             for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, x[i]);
-            top = max4(top);
-            const float mn = __builtin_fmaxf(m[rt], top);
+            const float mn = __builtin_fmaxf(m[rt], max4(top) * a.scale2);
             if (__builtin_amdgcn_ballot_w64(mn > m[rt])) {   // some row's maximum rose
                 const float f = weight_of(m[rt], mn);
                 l[rt] *= f;
@@ -281,82 +298,120 @@ __global__ __launch_bounds__(WK* WR * 64) void tree_attn_kernel(TreeArgs a) {
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                x[i] = __builtin_amdgcn_exp2f(x[i] - base);
+                x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.scale2, -base));
                 sum += x[i];
             }
             l[rt] += sum;   // this lane's keys; the four lanes of a row are added at the end
 #pragma unroll
             for (int j = 0; j < 4; ++j) pf[rt][j] = pack2<BF16>(x[2 * j], x[2 * j + 1]);
         }
-        // V: D/16 columns of this lane's eight keys.
-        constexpr int VW = D / 32;   // dwords of a key per lane
-        uint32_t vr[8][VW];
+        __builtin_amdgcn_sched_barrier(0);   // V is not read ahead of the scores: registers are short
+        // V: D/16 columns of this lane's eight keys, at most eight columns at a time.
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint8_t* const p = vt + (16 * (i >> 2) + 4 * g + (i & 3)) * D * 2 + c * VW * 4;
-            if constexpr (VW == 2) {
-                const u32x2_t v = *(const u32x2_t*)p;
-                vr[i][0] = v[0], vr[i][1] = v[1];
-            } else {
-#pragma unroll
-                for (int w = 0; w < VW; w += 4) {
-                    const u32x4_t v = *(const u32x4_t*)(p + 4 * w);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) vr[i][w + e] = v[e];
-                }
-            }
-        }
-        if (edge) {
-            // Keys past the end count as zeros.  A draft's infinity or NaN must
-            // not reach the rows that do not see it (0 * inf): it is taken out
-            // of the product and added, key by key, to the rows that do.
-            uint64_t odd[8];
+        for (int w0 = 0; w0 < VW; w0 += VH) {
+            uint32_t vr[8][VH];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int p = first + 16 * (i >> 2) + 4 * g + (i & 3);
-                bool bad = false;
+                const uint8_t* const p = vt + (16 * (i >> 2) + 4 * g + (i & 3)) * D * 2 + (c * VW + w0) * 4;
+                if constexpr (VH == 2) {
+                    const u32x2_t v = *(const u32x2_t*)p;
+                    vr[i][0] = v[0], vr[i][1] = v[1];
+                } else {
+                    const u32x4_t v = *(const u32x4_t*)p;
 #pragma unroll
-                for (int w = 0; w < VW; ++w) {
-                    const uint32_t v = p < total ? vr[i][w] : 0u;
-                    const bool lo = not_finite<BF16>(v), hi = not_finite<BF16>(v >> 16);
-                    bad |= p >= len && (lo || hi);
-                    vr[i][w] = p < len ? v : (lo ? 0u : v & 0xffffu) | (hi ? 0u : v & 0xffff0000u);
+                    for (int e = 0; e < 4; ++e) vr[i][e] = v[e];
                 }
-                odd[i] = __builtin_amdgcn_ballot_w64(bad);
             }
+            if constexpr (EDGE) {
+                // Keys past the end count as zeros.  A draft's infinity or NaN must
+                // not reach the rows that do not see it (0 * inf): it is taken out
+                // of the product, and given to the rows that do after the loop.
+                bool odd = false;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                for (int gk = 0; gk < 4 && odd[i]; ++gk) {
-                    if (!((odd[i] >> (16 * gk)) & 0xffff)) continue;
-                    const int j = 16 * (i >> 2) + 4 * gk + (i & 3), draft = first + j - len;
+                for (int i = 0; i < 8; ++i) {
+                    const int j = d0 + 16 * (i >> 2) + 4 * g + (i & 3);
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        const uint32_t pw = __shfl(pf[rt][i >> 1], 16 * gk + c);
-                        const float p = unpack1<BF16>(i & 1 ? pw >> 16 : pw & 0xffffu);
-                        const bool sees = (see[rt] >> (draft & 63)) & 1;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int d = 0; d < DT; ++d) {
-                                const uint32_t h = *(const uint16_t*)(vt + j * D * 2 + (DT * (4 * g + q) + d) * 2);
-                                if (sees && not_finite<BF16>(h)) o[rt][d][q] += p * unpack1<BF16>(h);
-                            }
+                    for (int w = 0; w < VH; ++w) {
+                        const uint32_t v = j < a.T ? vr[i][w] : 0u;
+                        const uint32_t out = j < 0 ? 0u : (not_finite<BF16>(v) ? 0xffffu : 0u) | (not_finite<BF16>(v >> 16) ? 0xffff0000u : 0u);
+                        odd |= out != 0;
+                        vr[i][w] = v & ~out;
                     }
                 }
+                if (__builtin_amdgcn_ballot_w64(odd)) any_odd = true;
+            }
+#pragma unroll
+            for (int d = 2 * w0; d < 2 * (w0 + VH); ++d) {
+                const int w = (d >> 1) - w0;
+                u32x4_t va;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    va[j] = __builtin_amdgcn_perm(vr[2 * j + 1][w], vr[2 * j][w], d & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) o[rt][d] = mfma<BF16>(va, pf[rt], o[rt][d]);
             }
         }
+    };
+
+    // NS - 1 tiles are under way ahead of the one that is multiplied.  A wave
+    // with a ring of its own asks for the next tile as soon as it has read the
+    // last; waves that share one do so after the barrier that also says that
+    // everybody's loads of this tile have arrived.
+    if (nt > 0) {
+        look_up(0);
+        wait_loads<0>();   // the rows have arrived: no load but the tiles' is waited for below
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            u32x4_t va;
+        for (int n = 0; n < NS - 1; ++n) issue(n);
+    }
+    auto step = [&](auto edge, int n) {
+        if constexpr (WR == 1) {
+            wait_loads<63>();   // LDS reads only
+            issue(n + NS - 1);
+            if (counted) wait_loads<(NS - 1) * 2 * kPer>();
+            else wait_loads<0>();
+        } else {
+            if (counted) wait_loads<(NS - 2) * 2 * kPer>();
+            else wait_loads<0>();
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (n >= nt) return;   // another group has one more
+            issue(n + NS - 1);
+        }
+        const uint8_t* const kt = ring + (n % NS) * kStage;
+        tile(edge, kt, kt + kHalf, first_of(n));
+    };
+    // Tiles of context alone, then those with drafts or the end inside.
+    const int context = min(t1, len / kTile) - t0 - kg;
+    const int plain = context > 0 ? (context + WK - 1) / WK : 0;
+    const int last = WR == 1 ? nt : loops;   // a barrier in each step: the same number for every group
+    int n = 0;
+    for (; n < plain; ++n) step(std::false_type{}, n);
+    for (; n < last; ++n) step(std::true_type{}, n);
+    wait_loads<0>();
+    __syncthreads();
+    if (any_odd) {
+        // Whatever its probability, a seen infinity makes its column infinite
+        // and a NaN makes it NaN: each is added as it is.
+#pragma unroll 1
+        for (int j = 0; j < a.T; ++j) {
+            const int p = len + j, at = p / kTile - t0;
+            if (at < 0 || at >= t1 - t0 || at % WK != kg) continue;   // another group's tile
+            const uint16_t* const vp = a.v + (long long)page_of(p) * a.page_stride + (long long)(p & page_mask) * a.token_stride + head;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                va[j] = __builtin_amdgcn_perm(vr[2 * j + 1][d >> 1], vr[2 * j][d >> 1], d & 1 ? 0x07060302u : 0x05040100u);
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) o[rt][d] = mfma<BF16>(va, pf[rt], o[rt][d]);
+                for (int d = 0; d < DT; d += 2) {
+                    const uint32_t v = *(const uint32_t*)(vp + DT * (4 * g + q) + d);
+                    const float lo = not_finite<BF16>(v) ? unpack1<BF16>(v & 0xffffu) : 0.f;
+                    const float hi = not_finite<BF16>(v >> 16) ? unpack1<BF16>(v >> 16) : 0.f;
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const bool sees = (see[rt] >> j) & 1;
+                        o[rt][d][q] += sees ? lo : 0.f, o[rt][d + 1][q] += sees ? hi : 0.f;
+                    }
+                }
         }
     }
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __syncthreads();
 
     // The groups' parts, each a sum with its own maximum: [group][row of the block].
     float* const ml = (float*)smem;                                  // [WK][kRows][2]
@@ -458,11 +513,20 @@ __global__ __launch_bounds__(256) void tree_merge_kernel(TreeArgs a, long long r
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] = 0.f;
     const float* const src = a.part_o + r * a.S * D + lane * C;
-    for (int s = 0; s < a.S; ++s) {
-        const float w = __shfl(f, s);
-        if (w == 0.f) continue;   // a part that saw nothing, or whose weight is 0
+    // Eight parts' loads at a time.  A part that saw nothing has weight 0 and
+    // zeros as its sums (an infinity in one that has not shows as it should).
+    for (int s = 0; s < a.S; s += 8) {
+        float x[8][C];
 #pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = __builtin_fmaf(w, src[(size_t)s * D + i], v[i]);
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < C; ++i) x[j][i] = s + j < a.S ? src[(size_t)(s + j) * D + i] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float w = __shfl(f, s + j);
+#pragma unroll
+            for (int i = 0; i < C; ++i) v[i] = s + j < a.S ? __builtin_fmaf(w, x[j][i], v[i]) : v[i];
+        }
     }
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
     const size_t at = out_row(a, unit / a.Hkv, unit % a.Hkv, row);
@@ -487,12 +551,12 @@ struct Plan {
     size_t ws;
 };
 
-template <int D, int RT, int WK, int WR>
+template <int D, int RT, int WK, int WR, int NS>
 void use(Plan& p) {
-    p.kernel[0] = tree_attn_kernel<false, D, RT, WK, WR>;
-    p.kernel[1] = tree_attn_kernel<true, D, RT, WK, WR>;
+    p.kernel[0] = tree_attn_kernel<false, D, RT, WK, WR, NS>;
+    p.kernel[1] = tree_attn_kernel<true, D, RT, WK, WR, NS>;
     p.rows = 16 * RT * WR, p.wk = WK, p.threads = 64 * WK * WR;
-    const size_t ring = (size_t)WK * 2 * 2 * kTile * D * 2;
+    const size_t ring = (size_t)WK * NS * 2 * kTile * D * 2;
     const size_t join = (size_t)WK * p.rows * (2 + (WK > 1 ? D : 0)) * sizeof(float);
     p.lds = ring > join ? ring : join;
 }
@@ -500,14 +564,13 @@ void use(Plan& p) {
 template <int D>
 void use_rows(Plan& p, int R) {
     if constexpr (D == 256) {
-        if (R <= 16) use<D, 1, 2, 1>(p);
-        else if (R <= 32) use<D, 1, 2, 2>(p);
-        else use<D, 1, 1, 4>(p);
+        if (R <= 16) use<D, 1, 2, 1, 2>(p);
+        else use<D, 1, 1, 4, 4>(p);
     } else {
-        if (R <= 16) use<D, 1, 4, 1>(p);
-        else if (R <= 32) use<D, 2, 4, 1>(p);
-        else if (R <= 64) use<D, 2, 2, 2>(p);
-        else use<D, 2, 1, 4>(p);
+        if (R <= 16) use<D, 1, 4, 1, 2>(p);
+        else if (R <= 32) use<D, 2, 4, 1, 2>(p);
+        else if (R <= 64) use<D, 2, 2, 2, 4>(p);
+        else use<D, 2, 1, 4, 4>(p);
     }
 }
 
@@ -577,7 +640,7 @@ extern "C" int tree_attn(const void* q, long long q_stride, const void* k, const
         (long long)table_stride * page_size < (long long)max_len + T)
         return W4A16_ERR_SHAPE;
     if (q_stride < (long long)Hq * D || q_stride % 8 || page_stride < 0 || token_stride < 0 || head_stride < 0 ||
-        page_stride % 8 || token_stride % 8 || head_stride % 8 || !(scale == scale) || scale - scale != 0.f)
+        (unsigned long long)page_size * (unsigned long long)token_stride >= (1ull << 30) || page_stride % 8 || token_stride % 8 || head_stride % 8 || !(scale == scale) || scale - scale != 0.f)
         return W4A16_ERR_SHAPE;
     if (!w4h::aligned16(q) || !w4h::aligned16(k) || !w4h::aligned16(v) || !w4h::aligned16(out) ||
         !w4h::aligned16(workspace) || ((uintptr_t)lens & 3) || ((uintptr_t)block_table & 3) ||
@@ -599,7 +662,8 @@ extern "C" int tree_attn(const void* q, long long q_stride, const void* k, const
     a.part_o = workspace ? (float*)(a.part_ml + (size_t)rows * p.S) : nullptr;
     a.q_stride = q_stride, a.page_stride = page_stride, a.token_stride = token_stride, a.head_stride = head_stride;
     a.num_pages = num_pages, a.page_shift = shift, a.table_stride = table_stride, a.max_len = max_len;
-    a.scale2 = scale * kLog2e;
+    a.scale2 = fmaxf(fabsf(scale) * kLog2e, 0x1p-126f);   // not 0: -inf marks what a row does not see
+    a.q_sign = scale < 0.f ? 0x80008000u : 0u;
     a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv, a.R = R, a.S = p.S, a.RB = p.RB;
     const bool bf16 = dtype == W4A16_BF16;
     allow_lds();

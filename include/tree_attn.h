@@ -43,7 +43,7 @@ extern "C" {
  * dtype       W4A16_F16 or W4A16_BF16, of q, k, v and out.  Products and sums
  *             are fp32; the probabilities take the dtype for the product with v.
  * Shape: B >= 1, 1 <= T <= 64, Hq a multiple of Hkv, D 64, 128 or 256,
- * page_size a power of two, 0 <= max_len <= 2^30, table_stride * page_size >=
+ * page_size a power of two with page_size * token_stride < 2^30, 0 <= max_len <= 2^30, table_stride * page_size >=
  * max_len + T.  max_len bounds lens (host knowledge: it sizes the split over the
  * keys; a captured graph stays valid for every lens up to it).  Deterministic
  * for the same lens.  workspace may be NULL where the query reports 0. */
