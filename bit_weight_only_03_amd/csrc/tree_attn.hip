@@ -359,10 +359,12 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
     // everybody's loads of this tile have arrived.
     if (nt > 0) {
         look_up(0);
-        wait_loads<0>();   // the rows have arrived: no load but the tiles' is waited for below
 #pragma unroll
         for (int n = 0; n < NS - 1; ++n) issue(n);
     }
+    // The rows have arrived: only tiles' loads are waited for in the loop.
+    if (counted && nt > 0) wait_loads<(NS - 1) * 2 * kPer>();
+    else wait_loads<0>();
     auto step = [&](auto edge, int n) {
         if constexpr (WR == 1) {
             wait_loads<63>();   // LDS reads only
@@ -490,52 +492,64 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
     }
 }
 
-// Joins the S parts of each row: o = sum 2^(m_s - top) o_s / sum 2^(m_s - top) l_s,
-// in order of s.  A wave per row: lane s holds part s's weight (S <= 64), then
-// every lane D/64 columns.
+// Joins the S parts of each row: o = sum 2^(m_s - top) o_s / sum 2^(m_s - top) l_s.
+// A workgroup per row: wave w adds parts w, w + 4, .. in that order (all loads
+// of eight parts under way at once), then the four sums are added in wave
+// order.  Bound by latency: a row's parts are a few KiB.
+constexpr int kMergeWaves = 4;
 template <bool BF16, int D>
-__global__ __launch_bounds__(256) void tree_merge_kernel(TreeArgs a, long long rows) {
-    constexpr int C = D / 64;
-    const int lane = threadIdx.x & 63;
-    const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (r >= rows) return;
+__global__ __launch_bounds__(kMergeWaves * 64) void tree_merge_kernel(TreeArgs a) {
+    constexpr int C = D / 64;   // columns per lane
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const size_t r = blockIdx.x;
     const int unit = (int)(r / a.R), row = (int)(r % a.R);
+    const float* const src = a.part_o + r * a.S * D + lane * C;
     float2 ml = float2{-__builtin_inff(), 0.f};
     if (lane < a.S) ml = a.part_ml[r * a.S + lane];
+    float x[8][C];
+    auto fetch = [&](int s0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int s = min(s0 + kMergeWaves * j, a.S - 1);   // past the end: a part that is not added
+#pragma unroll
+            for (int i = 0; i < C; ++i) x[j][i] = src[(size_t)s * D + i];
+        }
+    };
+    fetch(wave);
     float top = ml.x;
 #pragma unroll
     for (int s = 32; s >= 1; s >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, s));
-    const float f = weight_of(ml.x, top);
+    const float f = weight_of(ml.x, top);   // of part `lane`
     float sum = f * ml.y;
 #pragma unroll
     for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s);
     float v[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] = 0.f;
-    const float* const src = a.part_o + r * a.S * D + lane * C;
-    // Eight parts' loads at a time.  A part that saw nothing has weight 0 and
-    // zeros as its sums (an infinity in one that has not shows as it should).
-    for (int s = 0; s < a.S; s += 8) {
-        float x[8][C];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < C; ++i) x[j][i] = s + j < a.S ? src[(size_t)(s + j) * D + i] : 0.f;
+    for (int s0 = wave; s0 < a.S; s0 += 8 * kMergeWaves) {
+        if (s0 != wave) fetch(s0);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float w = __shfl(f, s + j);
+            const int s = s0 + kMergeWaves * j;
+            const float w = __shfl(f, s & 63);
 #pragma unroll
-            for (int i = 0; i < C; ++i) v[i] = s + j < a.S ? __builtin_fmaf(w, x[j][i], v[i]) : v[i];
+            for (int i = 0; i < C; ++i) v[i] = s < a.S ? __builtin_fmaf(w, x[j][i], v[i]) : v[i];
         }
     }
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    const size_t at = out_row(a, unit / a.Hkv, unit % a.Hkv, row);
+    __shared__ float parts[kMergeWaves][D];
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const uint32_t h = pack2<BF16>(v[i] * inv, 0.f);
-        ((uint16_t*)a.out)[at * D + lane * C + i] = (uint16_t)h;
+    for (int i = 0; i < C; ++i) parts[wave][lane * C + i] = v[i];
+    __syncthreads();
+    const size_t at = out_row(a, unit / a.Hkv, unit % a.Hkv, row);
+    const int d = threadIdx.x;
+    if (d < D) {
+        float o = parts[0][d];
+#pragma unroll
+        for (int w = 1; w < kMergeWaves; ++w) o += parts[w][d];
+        o *= sum == 0.f ? 0.f : 1.0f / sum;
+        ((uint16_t*)a.out)[at * D + d] = (uint16_t)pack2<BF16>(o, 0.f);
     }
-    if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -__builtin_inff() : (top - kLift<BF16> + __builtin_log2f(sum)) * kLn2;
+    if (d == 0 && a.lse) a.lse[at] = sum == 0.f ? -__builtin_inff() : (top - kLift<BF16> + __builtin_log2f(sum)) * kLn2;
 }
 
 typedef void (*kernel_t)(TreeArgs);
@@ -670,13 +684,10 @@ extern "C" int tree_attn(const void* q, long long q_stride, const void* k, const
     w4h::begin_launches();
     hipLaunchKernelGGL(p.kernel[bf16], dim3((unsigned)blocks), dim3(p.threads), p.lds, (hipStream_t)stream, a);
     if (p.S > 1) {
-        const dim3 grid((unsigned)((rows + 3) / 4));
-        if (D == 64)
-            hipLaunchKernelGGL((bf16 ? tree_merge_kernel<true, 64> : tree_merge_kernel<false, 64>), grid, dim3(256), 0, (hipStream_t)stream, a, rows);
-        else if (D == 128)
-            hipLaunchKernelGGL((bf16 ? tree_merge_kernel<true, 128> : tree_merge_kernel<false, 128>), grid, dim3(256), 0, (hipStream_t)stream, a, rows);
-        else
-            hipLaunchKernelGGL((bf16 ? tree_merge_kernel<true, 256> : tree_merge_kernel<false, 256>), grid, dim3(256), 0, (hipStream_t)stream, a, rows);
+        const kernel_t merge = D == 64    ? (bf16 ? tree_merge_kernel<true, 64> : tree_merge_kernel<false, 64>)
+                               : D == 128 ? (bf16 ? tree_merge_kernel<true, 128> : tree_merge_kernel<false, 128>)
+                                          : (bf16 ? tree_merge_kernel<true, 256> : tree_merge_kernel<false, 256>);
+        hipLaunchKernelGGL(merge, dim3((unsigned)rows), dim3(kMergeWaves * 64), 0, (hipStream_t)stream, a);
     }
     w4h::set_last_variant("tree_attn D=%d rows=%d groups=%d threads=%d blocks=%lld splits=%d row_blocks=%d lds=%zu", D,
                           p.rows, p.wk, p.threads, blocks, p.S, p.RB, p.lds);
