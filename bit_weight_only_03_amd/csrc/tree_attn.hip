@@ -90,6 +90,12 @@ __device__ __forceinline__ float unpack1(uint32_t h) {   // the low 16 bits
     return BF16 ? bitcast<float>(h << 16) : f16_bits_to_f32((uint16_t)h);
 }
 
+// Two 16-bit values: bit 15 of each half is set where its exponent is all ones (infinity, NaN).
+template <bool BF16>
+__device__ __forceinline__ uint32_t overflow(uint32_t v) {
+    return BF16 ? (v & 0x7f807f80u) + 0x00800080u : (v & 0x7c007c00u) + 0x04000400u;
+}
+
 template <bool BF16>
 __device__ __forceinline__ bool not_finite(uint32_t h) {
     constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
@@ -130,9 +136,10 @@ __device__ __forceinline__ float weight_of(float m, float top) {
     return m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - top);
 }
 
-// The address of a row's result, or null past the rows.
-__device__ __forceinline__ size_t out_row(const TreeArgs& a, int b, int kvh, int row) {
-    return ((size_t)b * a.T + row / a.G) * a.Hq + kvh * a.G + row % a.G;
+// The place of a row's result.
+__device__ __forceinline__ size_t out_row(const TreeArgs& a, uint32_t b, uint32_t kvh, uint32_t row) {
+    const uint32_t G = a.G;
+    return ((size_t)b * a.T + row / G) * a.Hq + kvh * G + row % G;
 }
 
 template <bool BF16, int D, int RT, int WK, int WR, int NS>
@@ -154,12 +161,14 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
 
     // Consecutive workgroups go to the XCDs in turn: the blocks of rows that
     // read the same keys sit 8 apart, on one XCD.
-    const int u8 = blockIdx.x >> 3, rb = u8 % a.RB, id = (u8 / a.RB) * 8 + (blockIdx.x & 7);
-    if (id >= a.B * a.Hkv * a.S) return;
-    const int split = id % a.S, unit = id / a.S, kvh = unit % a.Hkv, b = unit / a.Hkv;
+    const uint32_t u8 = blockIdx.x >> 3, row_blocks = a.RB, splits = a.S, heads = a.Hkv;
+    const uint32_t rb = u8 % row_blocks, id = (u8 / row_blocks) * 8 + (blockIdx.x & 7);
+    if (id >= a.B * heads * splits) return;
+    const uint32_t split = id % splits, unit = id / splits, kvh = unit % heads, b = unit / heads;
     const int len = min(max(a.lens[b], 0), a.max_len), total = len + a.T;
     const int tiles = (total + kTile - 1) / kTile;
-    const int t0 = (int)((long long)tiles * split / a.S), t1 = (int)((long long)tiles * (split + 1) / a.S);
+    // (tiles <= 2^25 + 2 and S <= 64: the products fit 32 bits.)
+    const int t0 = (uint32_t)tiles * split / (uint32_t)a.S, t1 = (uint32_t)tiles * (split + 1) / (uint32_t)a.S;
     const int nt = t1 - t0 > kg ? (t1 - t0 - kg + WK - 1) / WK : 0;   // this group's tiles
     const int loops = (t1 - t0 + WK - 1) / WK;                        // the same for every group (barriers)
 
@@ -234,11 +243,11 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
     uint64_t see[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int row = row0 + 16 * rt + c;
-        const bool there = row < a.R;
-        const int tok = there ? row / a.G : 0;
+        const uint32_t row = row0 + 16 * rt + c, G = a.G;
+        const bool there = (int)row < a.R;
+        const uint32_t tok = there ? row / G : 0u;
         see[rt] = there ? a.mask[(size_t)b * a.T + tok] & (~0ull >> (64 - a.T)) : 0;
-        const uint16_t* const qp = a.q + ((size_t)b * a.T + tok) * a.q_stride + (size_t)(kvh * a.G + (there ? row % a.G : 0)) * D;
+        const uint16_t* const qp = a.q + ((size_t)b * a.T + tok) * a.q_stride + (size_t)(kvh * G + (there ? row % G : 0u)) * D;
 #pragma unroll
         for (int s = 0; s < KS; ++s) qf[rt][s] = there ? *(const u32x4_t*)(qp + 32 * s + 8 * g) ^ a.q_sign : u32x4_t{0, 0, 0, 0};
     }
@@ -326,19 +335,28 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
                 // Keys past the end count as zeros.  A draft's infinity or NaN must
                 // not reach the rows that do not see it (0 * inf): it is taken out
                 // of the product, and given to the rows that do after the loop.
-                bool odd = false;
+                uint32_t odd = 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int j = d0 + 16 * (i >> 2) + 4 * g + (i & 3);
+                    const bool there = d0 + 16 * (i >> 2) + 4 * g + (i & 3) < a.T;
 #pragma unroll
                     for (int w = 0; w < VH; ++w) {
-                        const uint32_t v = j < a.T ? vr[i][w] : 0u;
-                        const uint32_t out = j < 0 ? 0u : (not_finite<BF16>(v) ? 0xffffu : 0u) | (not_finite<BF16>(v >> 16) ? 0xffff0000u : 0u);
-                        odd |= out != 0;
-                        vr[i][w] = v & ~out;
+                        vr[i][w] = there ? vr[i][w] : 0u;
+                        odd |= overflow<BF16>(vr[i][w]);
                     }
                 }
-                if (__builtin_amdgcn_ballot_w64(odd)) any_odd = true;
+                if (__builtin_amdgcn_ballot_w64((odd & 0x80008000u) != 0)) {
+                    any_odd = true;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const bool draft = d0 + 16 * (i >> 2) + 4 * g + (i & 3) >= 0;   // context goes in as it is
+#pragma unroll
+                        for (int w = 0; w < VH; ++w) {
+                            const uint32_t top = overflow<BF16>(vr[i][w]) & 0x80008000u;
+                            vr[i][w] &= draft ? ~((top >> 15) * 0xffffu) : ~0u;
+                        }
+                    }
+                }
             }
 #pragma unroll
             for (int d = 2 * w0; d < 2 * (w0 + VH); ++d) {
@@ -421,73 +439,65 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         l[rt] = sum4(l[rt]);
-        if (g == 0) {
+        if (WK > 1 && g == 0) {
             float* const at = ml + (kg * kRows + wr * RT * 16 + 16 * rt + c) * 2;
             at[0] = m[rt], at[1] = l[rt];
         }
     }
-    __syncthreads();
-    const size_t first_row = (size_t)unit * a.R;
+    if constexpr (WK > 1) __syncthreads();
+    // Where a row's sums (splits) or results go.
+    auto store4 = [&](size_t at, const float4_t& v) {
+        if (a.S > 1)
+            *(float4_t*)(a.part_o + at) = v;
+        else
+            *(u32x2_t*)((uint16_t*)a.out + at) = u32x2_t{pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3])};
+    };
+    auto row_at = [&](uint32_t row) {
+        return (a.S > 1 ? ((size_t)unit * a.R + row) * a.S + split : out_row(a, b, kvh, row)) * D;
+    };
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const int in_block = wr * RT * 16 + 16 * rt + c, row = rb * kRows + in_block;
-        float top = m[rt];
+        float top = m[rt], sum = WK > 1 ? 0.f : l[rt];
+        if constexpr (WK > 1) {
 #pragma unroll
-        for (int w = 0; w < WK; ++w) top = __builtin_fmaxf(top, ml[(w * kRows + in_block) * 2]);
-        float sum = 0.f;
+            for (int w = 0; w < WK; ++w) top = __builtin_fmaxf(top, ml[(w * kRows + in_block) * 2]);
 #pragma unroll
-        for (int w = 0; w < WK; ++w) {
-            const float* const at = ml + (w * kRows + in_block) * 2;
-            sum += weight_of(at[0], top) * at[1];
+            for (int w = 0; w < WK; ++w) {
+                const float* const at = ml + (w * kRows + in_block) * 2;
+                sum += weight_of(at[0], top) * at[1];
+            }
         }
         float f = weight_of(m[rt], top);
         if (a.S == 1) f = sum == 0.f ? 0.f : f / sum;
         if (kg == 0 && g == 0 && row < a.R) {
             if (a.S > 1)
-                a.part_ml[(first_row + row) * a.S + split] = float2{top, sum};
+                a.part_ml[((size_t)unit * a.R + row) * a.S + split] = float2{top, sum};
             else if (a.lse)
                 a.lse[out_row(a, b, kvh, row)] = sum == 0.f ? -__builtin_inff() : (top - kLift<BF16> + __builtin_log2f(sum)) * kLn2;
         }
+        // Lane (c, g) holds columns DT (4g + q) + d of its row.
+        float* const to = os + ((size_t)kg * kRows + in_block) * D;
+        const size_t at = row_at(row);
+        if (WK == 1 && row >= a.R) continue;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[rt][d][q] *= f;
-        // Lane c, g holds columns DT (4g + q) + d of its row.
-        if constexpr (WK > 1) {
-            float* const to = os + ((size_t)kg * kRows + in_block) * D;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int d = 0; d < DT; d += 4)
-                    *(float4_t*)(to + DT * (4 * g + q) + d) = float4_t{o[rt][d][q], o[rt][d + 1][q], o[rt][d + 2][q], o[rt][d + 3][q]};
-        } else if (row < a.R) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int d = 0; d < DT; d += 4) {
-                    const int col = DT * (4 * g + q) + d;
-                    if (a.S > 1)
-                        *(float4_t*)(a.part_o + ((first_row + row) * a.S + split) * D + col) =
-                            float4_t{o[rt][d][q], o[rt][d + 1][q], o[rt][d + 2][q], o[rt][d + 3][q]};
-                    else
-                        *(u32x2_t*)((uint16_t*)a.out + out_row(a, b, kvh, row) * D + col) =
-                            u32x2_t{pack2<BF16>(o[rt][d][q], o[rt][d + 1][q]), pack2<BF16>(o[rt][d + 2][q], o[rt][d + 3][q])};
-                }
-        }
+            for (int d = 0; d < DT; d += 4) {
+                const float4_t v = {o[rt][d][q] * f, o[rt][d + 1][q] * f, o[rt][d + 2][q] * f, o[rt][d + 3][q] * f};
+                if constexpr (WK > 1) *(float4_t*)(to + DT * (4 * g + q) + d) = v;
+                else store4(at + DT * (4 * g + q) + d, v);
+            }
     }
     if constexpr (WK > 1) {
         __syncthreads();
         for (int e = t * 4; e < kRows * D; e += WK * WR * 256) {
-            const int row = rb * kRows + e / D, col = e % D;
+            const int row = rb * kRows + e / D;
             if (row >= a.R) break;
             float4_t v = *(const float4_t*)(os + e);
 #pragma unroll
             for (int w = 1; w < WK; ++w) v += *(const float4_t*)(os + (size_t)w * kRows * D + e);
-            if (a.S > 1)
-                *(float4_t*)(a.part_o + ((first_row + row) * a.S + split) * D + col) = v;
-            else
-                *(u32x2_t*)((uint16_t*)a.out + out_row(a, b, kvh, row) * D + col) =
-                    u32x2_t{pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3])};
+            store4(row_at(row) + e % D, v);
         }
     }
 }
@@ -502,7 +512,7 @@ __global__ __launch_bounds__(kMergeWaves * 64) void tree_merge_kernel(TreeArgs a
     constexpr int C = D / 64;   // columns per lane
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const size_t r = blockIdx.x;
-    const int unit = (int)(r / a.R), row = (int)(r % a.R);
+    const uint32_t R = a.R, heads = a.Hkv, unit = blockIdx.x / R, row = blockIdx.x % R;
     const float* const src = a.part_o + r * a.S * D + lane * C;
     float2 ml = float2{-__builtin_inff(), 0.f};
     if (lane < a.S) ml = a.part_ml[r * a.S + lane];
@@ -531,7 +541,7 @@ __global__ __launch_bounds__(kMergeWaves * 64) void tree_merge_kernel(TreeArgs a
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int s = s0 + kMergeWaves * j;
-            const float w = __shfl(f, s & 63);
+            const float w = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(f), s & 63));
 #pragma unroll
             for (int i = 0; i < C; ++i) v[i] = s < a.S ? __builtin_fmaf(w, x[j][i], v[i]) : v[i];
         }
@@ -540,7 +550,7 @@ __global__ __launch_bounds__(kMergeWaves * 64) void tree_merge_kernel(TreeArgs a
 #pragma unroll
     for (int i = 0; i < C; ++i) parts[wave][lane * C + i] = v[i];
     __syncthreads();
-    const size_t at = out_row(a, unit / a.Hkv, unit % a.Hkv, row);
+    const size_t at = out_row(a, unit / heads, unit % heads, row);
     const int d = threadIdx.x;
     if (d < D) {
         float o = parts[0][d];
