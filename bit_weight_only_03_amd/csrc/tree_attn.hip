@@ -205,26 +205,29 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
     };
     auto of_k = [&](int page) { return make_rsrc(a.k + ((long long)page * a.page_stride + head), page_bytes); };
     auto of_v = [&](int page) { return make_rsrc(a.v + ((long long)page * a.page_stride + head), page_bytes); };
-    int pages[2];   // of the two halves of the tile that is issued next
-    auto look_up = [&](int n) {
-        const int p = first_of(n) + wr * kSpan;
-        pages[0] = pages[1] = page_of(p);
-        if (runs == 2) pages[1] = page_of(p + kSpan / 2);
+    struct Pages {
+        int half[2];
+    };
+    auto look_up = [&](int n) {   // the pages of the two halves of what this wave loads of tile n
+        const int p = first_of(min(n, nt - 1)) + wr * kSpan;
+        Pages pg;
+        pg.half[0] = page_of(p);
+        pg.half[1] = runs == 2 ? page_of(p + kSpan / 2) : pg.half[0];
+        return pg;
     };
     // Tile n (past the last one, the last one again: nothing reads it) into ring slot n.
-    auto issue = [&](int n) {
+    auto issue = [&](int n, const Pages& pg) {
         uint8_t* const to = ring + (n % NS) * kStage;
         const int first = first_of(min(n, nt - 1)) + wr * kSpan;
         if (runs) {
             uint32_t in_page = (uint32_t)(first & page_mask) * key_bytes;
-            __amdgpu_buffer_rsrc_t rk = of_k(pages[0]), rv = of_v(pages[0]);
+            __amdgpu_buffer_rsrc_t rk = of_k(pg.half[0]), rv = of_v(pg.half[0]);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                if (i == kPer / 2 && runs == 2) rk = of_k(pages[1]), rv = of_v(pages[1]), in_page = 0;
+                if (i == kPer / 2 && runs == 2) rk = of_k(pg.half[1]), rv = of_v(pg.half[1]), in_page = 0;
                 load(to, wr * kPer + i, rk, rv, row_lane, in_page);
                 in_page += kKeys * key_bytes;
             }
-            look_up(min(n + 1, nt - 1));
         } else {
             const int step = counted ? kKeys : page_mask + 1;
 #pragma unroll 1
@@ -243,13 +246,12 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
     uint64_t see[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const uint32_t row = row0 + 16 * rt + c, G = a.G;
-        const bool there = (int)row < a.R;
-        const uint32_t tok = there ? row / G : 0u;
-        see[rt] = there ? a.mask[(size_t)b * a.T + tok] & (~0ull >> (64 - a.T)) : 0;
-        const uint16_t* const qp = a.q + ((size_t)b * a.T + tok) * a.q_stride + (size_t)(kvh * G + (there ? row % G : 0u)) * D;
+        const uint32_t row = min(row0 + 16 * rt + c, a.R - 1), G = a.G;   // past the rows: the last one again, not stored
+        const uint32_t tok = row / G;
+        see[rt] = a.mask[(size_t)b * a.T + tok] & (~0ull >> (64 - a.T));
+        const uint16_t* const qp = a.q + ((size_t)b * a.T + tok) * a.q_stride + (size_t)(kvh * G + row % G) * D;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) qf[rt][s] = there ? *(const u32x4_t*)(qp + 32 * s + 8 * g) ^ a.q_sign : u32x4_t{0, 0, 0, 0};
+        for (int s = 0; s < KS; ++s) qf[rt][s] = *(const u32x4_t*)(qp + 32 * s + 8 * g);
     }
     bool any_odd = false;   // the same for the whole wave
     float4_t o[RT][DT];
@@ -314,7 +316,6 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) pf[rt][j] = pack2<BF16>(x[2 * j], x[2 * j + 1]);
         }
-        __builtin_amdgcn_sched_barrier(0);   // V is not read ahead of the scores: registers are short
         // V: D/16 columns of this lane's eight keys, at most eight columns at a time.
 #pragma unroll
         for (int w0 = 0; w0 < VW; w0 += VH) {
@@ -375,18 +376,27 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
     // with a ring of its own asks for the next tile as soon as it has read the
     // last; waves that share one do so after the barrier that also says that
     // everybody's loads of this tile have arrived.
+    Pages next{};   // of the tile that is issued next, asked for a step ahead
     if (nt > 0) {
-        look_up(0);
+        Pages pg[NS];
 #pragma unroll
-        for (int n = 0; n < NS - 1; ++n) issue(n);
+        for (int n = 0; n < NS; ++n) pg[n] = look_up(n);   // one latency for all
+#pragma unroll
+        for (int n = 0; n < NS - 1; ++n) issue(n, pg[n]);
+        next = pg[NS - 1];
     }
     // The rows have arrived: only tiles' loads are waited for in the loop.
     if (counted && nt > 0) wait_loads<(NS - 1) * 2 * kPer>();
     else wait_loads<0>();
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[rt][s] ^= a.q_sign;
     auto step = [&](auto edge, int n) {
         if constexpr (WR == 1) {
             wait_loads<63>();   // LDS reads only
-            issue(n + NS - 1);
+            issue(n + NS - 1, next);
+            next = look_up(n + NS);
             if (counted) wait_loads<(NS - 1) * 2 * kPer>();
             else wait_loads<0>();
         } else {
@@ -395,8 +405,10 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             if (n >= nt) return;   // another group has one more
-            issue(n + NS - 1);
+            issue(n + NS - 1, next);
+            next = look_up(n + NS);
         }
+        if (WR > 1 && row0 >= a.R) return;   // a wave without rows only loads
         const uint8_t* const kt = ring + (n % NS) * kStage;
         tile(edge, kt, kt + kHalf, first_of(n));
     };
