@@ -40,6 +40,7 @@ constexpr float kLn2 = 0x1.62e43p-1f;
 constexpr int kMaxSplit = 64;
 constexpr int kMaxDevices = 64;
 constexpr int kMaxDynamicLds = 160 * 1024;
+constexpr size_t kMaxWorkspace = (size_t)64 << 20;
 
 struct TreeArgs {
     const uint16_t* q;
@@ -597,36 +598,69 @@ void use(Plan& p) {
     p.lds = ring > join ? ring : join;
 }
 
+// The kernels of one head size: how their waves are arranged, and what a step
+// (a tile for each group) of a workgroup takes in microseconds, alone on its CU and beside a
+// second one, measured on MI355X with keys in HBM.
+struct Shape {
+    void (*use)(Plan&);
+    float alone, beside;
+};
 template <int D>
-void use_rows(Plan& p, int R) {
+const Shape* shapes(int& n) {
     if constexpr (D == 256) {
-        if (R <= 16) use<D, 1, 2, 1, 2>(p);
-        else use<D, 1, 1, 4, 4>(p);
+        static const Shape s[] = {{use<D, 1, 2, 1, 2>, 1.3f, 1.3f}, {use<D, 1, 1, 4, 4>, 1.1f, 1.1f}};
+        n = 2;
+        return s;
     } else {
-        if (R <= 16) use<D, 1, 4, 1, 2>(p);
-        else if (R <= 32) use<D, 2, 4, 1, 2>(p);
-        else if (R <= 64) use<D, 2, 2, 2, 4>(p);
-        else use<D, 2, 1, 4, 4>(p);
+        // D = 64 reads half the bytes a tile.
+        static const Shape s[] = {{use<D, 1, 4, 1, 2>, D == 64 ? 0.6f : 1.15f, D == 64 ? 0.75f : 1.15f},
+                                  {use<D, 2, 4, 1, 2>, D == 64 ? 0.75f : 1.25f, D == 64 ? 0.9f : 1.25f},
+                                  {use<D, 2, 2, 2, 4>, D == 64 ? 0.8f : 1.1f, D == 64 ? 1.0f : 1.1f},
+                                  {use<D, 2, 1, 4, 4>, D == 64 ? 0.7f : 0.85f, D == 64 ? 0.95f : 1.2f}};
+        n = 4;
+        return s;
     }
 }
+const Shape* shapes(int D, int& n) { return D == 64 ? shapes<64>(n) : D == 128 ? shapes<128>(n) : shapes<256>(n); }
 
+// The kernel and the split of the keys with the least estimated time.  Few rows
+// over many keys want many groups of keys, many rows a kernel whose waves share
+// the keys' tiles; a split fills the GPU but pays for its parts' traffic and the merge's
+// launch.  The estimate takes the longest request (max_len) for all of them.
 Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_len) {
-    Plan p{};
-    const int R = T * (Hq / Hkv);
-    if (D == 64) use_rows<64>(p, R);
-    else if (D == 128) use_rows<128>(p, R);
-    else use_rows<256>(p, R);
-    p.RB = (R + p.rows - 1) / p.rows;
-    p.units = (long long)B * Hkv;
-    // One workgroup or more per CU, each group of waves with two tiles at least.
-    const long long tiles = ((long long)max_len + T + kTile - 1) / kTile;
-    const int per_cu = (int)(kMaxDynamicLds / p.lds) < 2 ? 1 : 2;
-    long long S = (long long)w4h::cu_count() * per_cu / (p.units * p.RB);
-    S = S < kMaxSplit ? S : kMaxSplit;
-    S = S < tiles / (2 * p.wk) ? S : tiles / (2 * p.wk);
-    p.S = S < 1 ? 1 : (int)S;
-    p.ws = p.S > 1 ? w4h::ws_bytes((size_t)p.units * R * p.S * (D + 2) * sizeof(float)) : 0;
-    return p;
+    constexpr double kStart = 7.0, kMerge = 5.0, kPartBytesPerUs = 4e6;   // launch to first tile and last store; merge
+    const int R = T * (Hq / Hkv), cus = w4h::cu_count();
+    const long long units = (long long)B * Hkv, tiles = ((long long)max_len + T + kTile - 1) / kTile;
+    Plan best{};
+    double least = 0;
+    int n;
+    const Shape* const sh = shapes(D, n);
+    for (int i = 0; i < n; ++i) {
+        Plan p{};
+        sh[i].use(p);
+        p.units = units;
+        p.RB = (R + p.rows - 1) / p.rows;
+        const int occupancy = p.lds * 2 <= (size_t)kMaxDynamicLds ? 2 : 1;
+        // Splits worth a look: none, few, and those that fill every CU once or to its occupancy, or halfway.
+        const long long full = cus / (units * p.RB), most = (long long)cus * occupancy / (units * p.RB);
+        for (long long S : {1LL, 2LL, 3LL, full / 2, full, most}) {
+            S = S < kMaxSplit ? S : kMaxSplit;
+            S = S < tiles / (2 * p.wk) ? S : tiles / (2 * p.wk);   // two tiles at least for each group
+            S = S < 1 ? 1 : S;
+            p.ws = S > 1 ? w4h::ws_bytes((size_t)units * R * S * (D + 2) * sizeof(float)) : 0;
+            if (p.ws > kMaxWorkspace) continue;
+            const double wgs = (double)units * p.RB * S, steps = ceil((double)tiles / S / p.wk);
+            const double rounds = ceil(wgs / ((double)cus * occupancy));
+            double t = rounds * (kStart + steps * (wgs > cus ? sh[i].beside : sh[i].alone));
+            if (S > 1) t += kMerge + (double)units * R * S * D * 8 / kPartBytesPerUs;
+            if (best.rows == 0 || t < least) {
+                least = t;
+                best = p;
+                best.S = (int)S;
+            }
+        }
+    }
+    return best;
 }
 
 // The kernels' dynamic LDS may pass the default limit: said once per process and device.
@@ -634,15 +668,16 @@ void allow_lds() {
     static std::atomic<bool> done[kMaxDevices];
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices || done[dev].load(std::memory_order_acquire)) return;
-    for (int D : {64, 128, 256})
-        for (int R : {1, 17, 33, 65}) {
-            Plan q{};
-            if (D == 64) use_rows<64>(q, R);
-            else if (D == 128) use_rows<128>(q, R);
-            else use_rows<256>(q, R);
-            for (kernel_t k : q.kernel)
+    for (int D : {64, 128, 256}) {
+        int n;
+        const Shape* const sh = shapes(D, n);
+        for (int i = 0; i < n; ++i) {
+            Plan p{};
+            sh[i].use(p);
+            for (kernel_t k : p.kernel)
                 (void)hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicLds);
         }
+    }
     done[dev].store(true, std::memory_order_release);
 }
 
