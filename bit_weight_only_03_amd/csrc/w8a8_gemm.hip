@@ -17,6 +17,8 @@
 // Lane l of an operand holds row l & 15 and the chunks l >> 4 and 4 + (l >> 4)
 // of its 128 bytes.  Which k an MFMA slot stands for does not matter as long as
 // both operands agree.
+#include <math.h>
+
 #include <atomic>
 
 #include "w8a8_common.h"
@@ -272,7 +274,7 @@ __global__ __launch_bounds__(W * 64) void w8a8_skinny_kernel(GemmArgs a) {
 // (r >> 2) WN/4 + 4 t + (r & 3): a lane's results over all tiles are then WN/4
 // consecutive columns of one row of y, stored 16 bytes at a time.  The key of
 // such a row follows r & 7, as its 8 neighbouring lanes need.
-template <int BM, int BN, int WGM, int WGN>
+template <int BM, int BN, int WGM, int WGN, int XD>
 __global__ __launch_bounds__(WGM * WGN * 64) void w8a8_tiled_kernel(GemmArgs a) {
     constexpr int W = WGM * WGN, WM = BM / WGM, WN = BN / WGN, MT = WM / 16, NT = WN / 16;
     constexpr int kXBuf = BM * kStepK, kWBuf = BN * kStepK;
@@ -314,13 +316,13 @@ __global__ __launch_bounds__(WGM * WGN * 64) void w8a8_tiled_kernel(GemmArgs a) 
 #pragma unroll
     for (int j = 0; j < WL; ++j) woff[j] = (uint32_t)(8 * (j * W + wave) + row8) * K + 16u * wchunk;
 
-    // Load j of this wave: of block b of x into ring slot i (of 2), of w into slot i (of 3).
+    // Load j of this wave: of block b of x into ring slot i (of XD), of w into slot i (of 3).
     auto issue_x = [&](int j, int b, int i) {
         load_lds(rx, smem + i * kXBuf + (j * W + wave) * 1024, b == last && 16 * xchunk >= tail ? kOutside : xoff[j],
                  (uint32_t)b * kStepK);
     };
     auto issue_w = [&](int j, int b, int i) {
-        load_lds(rw, smem + 2 * kXBuf + i * kWBuf + (j * W + wave) * 1024,
+        load_lds(rw, smem + XD * kXBuf + i * kWBuf + (j * W + wave) * 1024,
                  b == last && 16 * wchunk >= tail ? kOutside : woff[j], (uint32_t)b * kStepK);
     };
 
@@ -343,39 +345,51 @@ __global__ __launch_bounds__(WGM * WGN * 64) void w8a8_tiled_kernel(GemmArgs a) 
         for (int m = 0; m < MT; ++m)
             sx[m] = bitcast<float>(__builtin_amdgcn_raw_buffer_load_b32(rxs, xs_off + 64u * m, 0, 0));
     };
-    scales(b0);
+    // Loads are waited for by their number, in the order of the steps: x and w
+    // of a block, then (XD = 3) the next block's scales, x and w, or (XD = 2) the next w.
+    const int second = min(b0 + 1, b1 - 1);
+    if constexpr (XD == 2) scales(b0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < XL; ++j) issue_x(j, b0, 0);
 #pragma unroll
     for (int j = 0; j < WL; ++j) issue_w(j, b0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (XD == 3) {
+        scales(b0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < WL; ++j) issue_w(j, min(b0 + 1, b1 - 1), 1);
+        for (int j = 0; j < XL; ++j) issue_x(j, second, 1);
+    }
+#pragma unroll
+    for (int j = 0; j < WL; ++j) issue_w(j, second, 1);
     __builtin_amdgcn_sched_barrier(0);
     float s[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) s[m] = sx[m] * sw;
     const uint8_t* const xl = smem + (wm * WM + c) * kStepK;
-    const uint8_t* const wl = smem + 2 * kXBuf + (wn * WN + (c >> 2) * (WN / 4) + (c & 3)) * kStepK;
+    const uint8_t* const wl = smem + XD * kXBuf + (wn * WN + (c >> 2) * (WN / 4) + (c & 3)) * kStepK;
     int xs = 0, ws3 = 0;
+    constexpr int kYounger = XD == 2 ? WL : XL + WL + MT + 1;   // loads issued after this block's last
     for (int b = b0; b < b1; ++b) {
-        // This wave's loads of this block have arrived (those of the next
-        // block of w may still be on their way) and its reads of the last
-        // block are done; after the barrier that holds for every wave.
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(WL) : "memory");
+        // This wave's loads of this block have arrived (younger ones may still
+        // be on their way) and its reads of the last block are done; after the
+        // barrier that holds for every wave.
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kYounger) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         const uint8_t* const xb = xl + xs * kXBuf;
         const uint8_t* const wb = wl + ws3 * kWBuf;
-        xs ^= 1;
-        const int fill = ws3 == 0 ? 2 : ws3 - 1;
+        // The slots read in the last step take the loads of this one.
+        const int xfill = xs == 0 ? XD - 1 : xs - 1, wfill = ws3 == 0 ? 2 : ws3 - 1;
+        xs = xs == XD - 1 ? 0 : xs + 1;
         ws3 = ws3 == 2 ? 0 : ws3 + 1;
         i32x8_t xf[MT], wf[2];
         wf[0] = operand(wb, g, key);
 #pragma unroll
         for (int m = 0; m < MT; ++m) xf[m] = operand(xb + 16 * m * kStepK, g, key);
         // The next step's loads; the last step repeats its own, which nothing reads.
-        const int next = min(b + 1, b1 - 1), next2 = min(b + 2, b1 - 1);
+        const int next = min(b + 1, b1 - 1), next2 = min(b + 2, b1 - 1), nextx = XD == 3 ? next2 : next;
         scales(next);
         __builtin_amdgcn_sched_barrier(0);
         // The block sums of kLag products are under way while an older one is scaled and added.
@@ -392,8 +406,8 @@ __global__ __launch_bounds__(WGM * WGN * 64) void w8a8_tiled_kernel(GemmArgs a) 
 #pragma unroll
                     for (int i = 0; i < kAll; ++i) {
                         if (i < lo || i >= hi) continue;
-                        if (i < XL) issue_x(i, next, xs);
-                        else issue_w(i - XL, next2, fill);
+                        if (i < XL) issue_x(i, nextx, xfill);
+                        else issue_w(i - XL, next2, wfill);
                     }
                 }
                 d[j % (kLag + 1)] = mfma_block(wf[n & 1], xf[m]);
@@ -448,76 +462,99 @@ struct Plan {
 };
 
 template <int MT, int XR, int NT, int RD, int W>
-void use_skinny(Plan& p, const char* name) {
+Plan skinny_plan(const char* name) {
+    Plan p{};
     p.kernel = w8a8_skinny_kernel<MT, XR, NT, RD, W>;
     p.name = name;
     p.bm = XR, p.bn = 16 * NT, p.threads = W * 64;
     p.lds = (size_t)W * RD * (16 * NT + XR) * kStepK + kTableFloats * sizeof(float);
     p.floats = 16 * MT * 16 * NT;
+    return p;
 }
 
-template <int BM, int BN, int WGM, int WGN>
-void use_tiled(Plan& p, const char* name) {
-    p.kernel = w8a8_tiled_kernel<BM, BN, WGM, WGN>;
+template <int BM, int BN, int WGM, int WGN, int XD>
+Plan tiled_plan(const char* name) {
+    Plan p{};
+    p.kernel = w8a8_tiled_kernel<BM, BN, WGM, WGN, XD>;
     p.name = name;
     p.bm = BM, p.bn = BN, p.threads = WGM * WGN * 64;
-    p.lds = (size_t)(2 * BM + 3 * BN) * kStepK;
+    p.lds = (size_t)(XD * BM + 3 * BN) * kStepK;
     p.floats = BM * BN;
+    return p;
 }
 
 constexpr size_t kMaxPartials = (size_t)64 << 20;
 constexpr int kCounters = (int)(w4h::kWsHead / sizeof(unsigned));
 
-// Slices of K so that tiles * S workgroups fill the GPU, each keeping at
-// least min_units units, within the workspace's counters and kMaxPartials.
-int more_slices(const Plan& p, int kb, int S, long long want, int min_units) {
-    const long long tiles = p.tiles_m * p.tiles_n;
-    while (tiles * S * 2 <= want && kb / (2 * S) >= min_units && 2 * S <= kMaxSplit && tiles <= kCounters &&
-           (size_t)tiles * 2 * S * p.floats * sizeof(float) <= kMaxPartials)
-        S *= 2;
-    return S;
-}
+// The kernels, each with what a step takes in microseconds (128 k of a tile; a
+// unit for each of the four waves), alone on its CU and beside a second workgroup, what a
+// launch takes besides, and the rate at which it streams w from HBM (bytes per
+// microsecond: a tile's rows are read 128 bytes at a time, the skinny
+// kernels' 512).  Measured on MI355X, K = 5120 and 17408, N = 1024 .. 34816.
+// Kernels for far fewer or more rows than M are not looked at (from, to).
+struct Kernel {
+    Plan p;   // all but the counts of tiles, slices and bytes
+    int from, to;
+    bool skinny;
+    float alone, beside, start, stream;
+};
+const Kernel kKernels[] = {
+    {skinny_plan<1, 8, 1, 4, 4>("skinny8x16"), 1, 8, true, 0.27f, 0.45f, 4.0f, 7.0e6f},
+    {skinny_plan<1, 8, 2, 3, 4>("skinny8x32"), 1, 8, true, 0.42f, 0.60f, 4.5f, 7.0e6f},
+    {skinny_plan<1, 16, 2, 3, 4>("skinny16x32"), 9, 16, true, 0.58f, 0.75f, 4.5f, 7.0e6f},
+    {skinny_plan<2, 32, 2, 2, 4>("skinny32x32"), 17, 64, true, 0.78f, 1.10f, 4.5f, 7.0e6f},
+    {tiled_plan<64, 128, 2, 2, 2>("tiled64x128"), 17, 512, false, 0.53f, 0.79f, 6.0f, 3.3e6f},
+    {tiled_plan<128, 128, 2, 2, 2>("tiled128x128"), 65, 1 << 26, false, 0.78f, 1.15f, 6.0f, 3.3e6f},
+    {tiled_plan<128, 256, 2, 4, 3>("tiled128x256"), 65, 1 << 26, false, 0.97f, 0.97f, 7.0f, 3.3e6f},
+    {tiled_plan<256, 256, 4, 2, 2>("tiled256x256"), 257, 1 << 26, false, 1.60f, 1.60f, 8.0f, 3.3e6f},
+};
+constexpr int kKernelCount = sizeof kKernels / sizeof kKernels[0];
 
+// The kernel and the slices of K with the least estimated time: rounds of
+// workgroups over the CUs, each a start and its steps, not faster than w
+// arrives; slices add their partial sums' traffic and the merge.
 Plan make_plan(int M, int N, int K) {
-    Plan p{};
     const int kb = (K + kStepK - 1) / kStepK, cus = w4h::cu_count();
-    auto count = [&] {
+    const int only = w4h::overrides().w8_variant, slices = w4h::overrides().w8_split;
+    Plan best{};
+    float least = 0;
+    for (int v = 0; v < kKernelCount; ++v) {
+        const Kernel& k = kKernels[v];
+        if (only >= 0 && only < kKernelCount ? v != only : (M < k.from || M > k.to)) continue;
+        Plan p = k.p;
         p.tiles_m = (M + p.bm - 1) / p.bm;
         p.tiles_n = (N + p.bn - 1) / p.bn;
-    };
-    int v = w4h::overrides().w8_variant;
-    if (v < 0) v = M <= 8 ? 0 : M <= 16 ? 1 : M <= 32 ? 2 : M <= 64 ? 3 : M <= 512 ? 10 : 11;
-    bool skinny = v < 10;
-    int S = 1;
-    if (skinny) {
-        switch (v) {
-            case 0: use_skinny<1, 8, 1, 3, 8>(p, "skinny8"); break;
-            case 1: use_skinny<1, 16, 1, 2, 8>(p, "skinny16"); break;
-            case 2: use_skinny<2, 32, 1, 3, 4>(p, "skinny32"); break;
-            default: use_skinny<4, 64, 1, 3, 4>(p, "skinny64"); break;
+        const long long all = p.tiles_m * p.tiles_n;
+        const int tiles = all < (1 << 24) ? (int)all : 1 << 24;   // more never has slices
+        const int waves = k.skinny ? p.threads / 64 : 1;          // units a step takes
+        const int slots = 2 * p.lds <= (size_t)kMaxDynamicLds ? 2 * cus : cus;
+        // The products of scales of a skinny kernel's slice fit its table.
+        const int least_S = k.skinny ? (kb * p.bm + kTableFloats - 1) / kTableFloats : 1;
+        int last = 0;
+        for (int S : {1, 2, 4, 8, cus / tiles / 2, cus / tiles, slots / tiles}) {
+            S = slices > 0 ? slices : S;
+            S = S < kb / (2 * waves) ? S : kb / (2 * waves);   // two steps at least
+            S = S < least_S ? least_S : S;
+            S = S < 1 ? 1 : S > kMaxSplit ? kMaxSplit : S;
+            if (S <= last) continue;
+            last = S;
+            if (k.skinny && ((kb + S - 1) / S) * p.bm > kTableFloats) continue;
+            const size_t partials = S > 1 ? (size_t)tiles * S * p.floats * sizeof(float) : 0;
+            if (S > 1 && (tiles > kCounters || partials > kMaxPartials)) continue;
+            const float wgs = (float)all * S, steps = (float)((kb + S * waves - 1) / (S * waves));
+            float t = ceilf(wgs / slots) * (k.start + steps * (wgs > cus ? k.beside : k.alone));
+            t = fmaxf(t, k.start + (float)N * K / k.stream);
+            if (S > 1) t += 2.0f + 0.3f * S + partials / 2e6f;
+            if (best.S == 0 || t < least) {
+                least = t;
+                best = p;
+                best.S = S;
+                best.ws = w4h::ws_bytes(partials);
+                best.blocks = k.skinny ? (p.tiles_n * S + 7) / 8 * 8 * p.tiles_m : (all * S + 7) / 8 * 8;
+            }
         }
-        count();
-        // A slice's products of scales fit the workgroup's table.
-        while (((kb + S - 1) / S) * p.bm > kTableFloats) S *= 2;
-        const long long tiles = p.tiles_m * p.tiles_n;
-        if (S > kMaxSplit || (S > 1 && (tiles > kCounters ||
-                                        (size_t)tiles * S * p.floats * sizeof(float) > kMaxPartials)))
-            skinny = false;
-        else
-            S = more_slices(p, kb, S, 4LL * cus, 8);
     }
-    if (!skinny) {
-        if (v == 11) use_tiled<256, 256, 4, 2>(p, "tiled256");
-        else use_tiled<128, 128, 2, 2>(p, "tiled128");
-        count();
-        S = more_slices(p, kb, 1, 2LL * cus, 8);
-    }
-    if (w4h::overrides().w8_split > 0) S = w4h::overrides().w8_split;
-    p.S = S;
-    const long long tiles = p.tiles_m * p.tiles_n;
-    p.ws = S > 1 ? w4h::ws_bytes((size_t)tiles * S * p.floats * sizeof(float)) : 0;
-    p.blocks = skinny ? (p.tiles_n * S + 7) / 8 * 8 * p.tiles_m : (tiles * S + 7) / 8 * 8;
-    return p;
+    return best;
 }
 
 // The kernels' dynamic LDS may pass the default limit: said once per process and device.
@@ -526,10 +563,8 @@ void allow_lds() {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices || done[dev].load(std::memory_order_acquire))
         return;
-    for (const void* k : {(const void*)w8a8_skinny_kernel<1, 8, 1, 3, 8>, (const void*)w8a8_skinny_kernel<1, 16, 1, 2, 8>,
-                          (const void*)w8a8_skinny_kernel<2, 32, 1, 3, 4>, (const void*)w8a8_skinny_kernel<4, 64, 1, 3, 4>,
-                          (const void*)w8a8_tiled_kernel<128, 128, 2, 2>, (const void*)w8a8_tiled_kernel<256, 256, 4, 2>})
-        (void)hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicLds);
+    for (const Kernel& k : kKernels)
+        (void)hipFuncSetAttribute((const void*)k.p.kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicLds);
     done[dev].store(true, std::memory_order_release);
 }
 
