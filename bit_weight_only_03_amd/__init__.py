@@ -102,7 +102,9 @@ def _lib_get():
 
 class _LazyLib:
     def __getattr__(self, name):
-        return getattr(_lib_get(), name)
+        f = getattr(_lib_get(), name)
+        setattr(self, name, f)   # found without this detour from now on
+        return f
 
 
 _lib = _LazyLib()

@@ -44,18 +44,26 @@ __device__ __forceinline__ uint32_t pk_f16(float a, float b) {
     return as_u(half2_t{(_Float16)a, (_Float16)b});
 }
 
+// A store that need not stay in the caches (NT), or an ordinary one.
+template <bool NT, typename V>
+__device__ __forceinline__ void store(V* p, const V& v) {
+    if constexpr (NT) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
 // Eight fp32 values stored in the dtype (16-bit types rounded to nearest even).
+template <bool NT = false>
 __device__ __forceinline__ void store8(void* p, int dtype, size_t o, const float* f) {
     if (dtype == W4A16_F32) {
-        *(float4_t*)((float*)p + o) = float4_t{f[0], f[1], f[2], f[3]};
-        *(float4_t*)((float*)p + o + 4) = float4_t{f[4], f[5], f[6], f[7]};
+        store<NT>((float4_t*)((float*)p + o), float4_t{f[0], f[1], f[2], f[3]});
+        store<NT>((float4_t*)((float*)p + o + 4), float4_t{f[4], f[5], f[6], f[7]});
         return;
     }
     u32x4_t v;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         v[j] = dtype == W4A16_F16 ? pk_f16(f[2 * j], f[2 * j + 1]) : pk_bf16(f[2 * j], f[2 * j + 1]);
-    *(u32x4_t*)((uint16_t*)p + o) = v;
+    store<NT>((u32x4_t*)((uint16_t*)p + o), v);
 }
 
 // v of another lane of the same 16 (a DPP row), by DPP control word.
@@ -82,6 +90,7 @@ __device__ __forceinline__ float block_scale(const float* n) {
 // Eight values over the scale as e4m3, rounded to nearest even.  |n| / s is at
 // most 448 but for the rounding of the quotient, which stays below 464, where
 // e4m3 still rounds to 448.
+template <bool NT>
 __device__ __forceinline__ void store_q8(uint8_t* p, const float* n, float s) {
     const float r = __builtin_amdgcn_rcpf(s);
     u32x2_t v;
@@ -91,7 +100,7 @@ __device__ __forceinline__ void store_q8(uint8_t* p, const float* n, float s) {
         w = __builtin_amdgcn_cvt_pk_fp8_f32(n[4 * j + 2] * r, n[4 * j + 3] * r, w, true);
         v[j] = (uint32_t)w;
     }
-    *(u32x2_t*)p = v;
+    store<NT>((u32x2_t*)p, v);
 }
 
 }  // namespace w4k

@@ -34,12 +34,18 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-// One row per workgroup, P vectors of 8 columns per lane: vector p of lane t
-// is number p * blockDim.x + t, so a wave's loads are contiguous and a block
-// of 128 columns stays inside 16 lanes (blockDim.x is a multiple of 64).
-// K / 8 vectors do not fill the last ones; those lanes load nothing and add
-// zeros.
-template <int P>
+// P vectors of 8 columns per lane: vector p of the row's lane t is number
+// p * threads + t, so a wave's loads are contiguous and a block of 128 columns
+// stays inside 16 lanes (threads is a multiple of 64).  Where K / 8 vectors do
+// not fill the last ones, those lanes load nothing and add zeros.  A row per
+// workgroup, its waves' sums joined through LDS (a wave per row and four rows
+// per workgroup took as long for K = 256 .. 1024).  NT: results bypass the
+// caches' retention where they are larger than what the next kernel could find
+// there (2560 x 16384: 58 against 64 us; 8192 x 5120: 70 against 72).
+// Bound by memory: 8192 x 5120 with residual moves 294 MB in 67 us, 4.4 TB/s,
+// where a 1 GiB copy reaches 4.8.  More vectors per lane and fewer waves were
+// slower (P = 2: 70, 4: 84, 10: 103 us): they only delay the first store.
+template <int P, bool NT>
 __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormArgs a) {
     const int t = threadIdx.x, threads = blockDim.x;
     const size_t row = blockIdx.x;
@@ -69,7 +75,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormArgs a) {
             const int v = p * threads + t;
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[p][e] += r[p][e];
-            if (a.h && v < nv) store8(a.h, a.residual_dtype, row * a.K + 8 * (size_t)v, h[p]);
+            if (a.h && v < nv) store8<NT>(a.h, a.residual_dtype, row * a.K + 8 * (size_t)v, h[p]);
         }
     }
     float ss = 0.f;
@@ -90,12 +96,12 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormArgs a) {
         float n[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) n[e] = h[p][e] * rstd * w[p][e];
-        if (a.y && v < nv) store8(a.y, a.y_dtype, row * a.K + 8 * (size_t)v, n);
+        if (a.y && v < nv) store8<NT>(a.y, a.y_dtype, row * a.K + 8 * (size_t)v, n);
         if (a.q) {
             // Lanes past the row's end hold zeros: they leave the maximum as it is.
             const float s = block_scale(n);
             if (v < nv) {
-                store_q8(a.q + row * a.K + 8 * (size_t)v, n, s);
+                store_q8<NT>(a.q + row * a.K + 8 * (size_t)v, n, s);
                 if ((t & 15) == 0) a.scales[(size_t)(v >> 4) * a.M + row] = s;
             }
         }
@@ -127,16 +133,21 @@ struct GatedArgs {
     int x_dtype, y_dtype;
     int M, K;
     int chunks;   // workgroups per row
+    int shift;    // log2 of the lanes that take a row
 };
 
 constexpr int kGatedThreads = 256;
 constexpr int kGatedCols = kGatedThreads * 8;
 
-// A workgroup takes 2048 columns of one row; a block of 128 columns is 16 lanes.
+// A workgroup takes 2048 columns of one row, or several short rows (a power of
+// two of lanes each, 16 at least); a block of 128 columns is 16 lanes.  Bound by
+// memory: 4096 x 17408 moves 359 MB in 65 us, 5.5 TB/s.
+template <bool NT>
 __global__ __launch_bounds__(kGatedThreads) void silu_mul_quant_kernel(GatedArgs a) {
-    const size_t row = blockIdx.x / (unsigned)a.chunks;
-    const int chunk = blockIdx.x % (unsigned)a.chunks;
-    const int k = chunk * kGatedCols + (int)threadIdx.x * 8;
+    const unsigned chunk = blockIdx.x % (unsigned)a.chunks;
+    const size_t row = (size_t)(blockIdx.x / (unsigned)a.chunks) * (kGatedThreads >> a.shift) + (threadIdx.x >> a.shift);
+    if (row >= (size_t)a.M) return;   // whole blocks of lanes
+    const int k = chunk * kGatedCols + (int)(threadIdx.x & ((1u << a.shift) - 1)) * 8;
     float g[8], u[8], n[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = u[e] = 0.f;
@@ -146,11 +157,11 @@ __global__ __launch_bounds__(kGatedThreads) void silu_mul_quant_kernel(GatedArgs
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) n[e] = silu(g[e]) * u[e];
-    if (a.y && k < a.K) store8(a.y, a.y_dtype, row * a.K + k, n);
+    if (a.y && k < a.K) store8<NT>(a.y, a.y_dtype, row * a.K + k, n);
     if (a.q) {
         const float s = block_scale(n);
         if (k < a.K) {
-            store_q8(a.q + row * a.K + k, n, s);
+            store_q8<NT>(a.q + row * a.K + k, n, s);
             if ((threadIdx.x & 15) == 0) a.scales[(size_t)(k >> 7) * a.M + row] = s;
         }
     }
@@ -158,6 +169,7 @@ __global__ __launch_bounds__(kGatedThreads) void silu_mul_quant_kernel(GatedArgs
 
 bool dtype_ok(int d) { return d == W4A16_F16 || d == W4A16_BF16 || d == W4A16_F32; }
 
+constexpr size_t kStreamElements = (size_t)16 << 20;   // results from here on are stored past the caches
 constexpr int kMaxThreads = 1024;
 constexpr int kMaxNormPasses = 4;
 constexpr int kMaxNormK = kMaxThreads * 8 * kMaxNormPasses;
@@ -190,10 +202,13 @@ extern "C" int w8a8_rmsnorm_quant(const void* x, int x_dtype, long long ldx, con
     NormArgs a{x, residual, weight, h_out, y_out, (uint8_t*)q, scales, ldx, x_dtype,
                residual_dtype, weight_dtype, y_dtype, M, K, eps};
     const int nv = K / 8;
+    const bool nt = (size_t)M * K >= kStreamElements;
     const int P = nv <= kMaxThreads ? 1 : nv <= 2 * kMaxThreads ? 2 : 4;
     const int threads = (((nv + P - 1) / P) + 63) / 64 * 64;
+    auto kernel = P == 1   ? (nt ? rmsnorm_quant_kernel<1, true> : rmsnorm_quant_kernel<1, false>)
+                  : P == 2 ? (nt ? rmsnorm_quant_kernel<2, true> : rmsnorm_quant_kernel<2, false>)
+                           : (nt ? rmsnorm_quant_kernel<4, true> : rmsnorm_quant_kernel<4, false>);
     w4h::begin_launches();
-    auto kernel = P == 1 ? rmsnorm_quant_kernel<1> : P == 2 ? rmsnorm_quant_kernel<2> : rmsnorm_quant_kernel<4>;
     hipLaunchKernelGGL(kernel, dim3(M), dim3(threads), 0, (hipStream_t)stream, a);
     w4h::set_last_variant("w8a8_rmsnorm passes=%d threads=%d rows=%d", P, threads, M);
     return w4h::launch_status();
@@ -209,10 +224,14 @@ extern "C" int w8a8_silu_mul_quant(const void* x, int x_dtype, long long ldx, vo
     if (int rc = check_out(y_out, y_dtype, q, scales)) return rc;
     const long long chunks = (K + kGatedCols - 1) / kGatedCols;
     if (chunks * M > 0x7fffffffLL) return W4A16_ERR_SHAPE;
-    GatedArgs a{x, y_out, (uint8_t*)q, scales, ldx, x_dtype, y_dtype, M, K, (int)chunks};
+    int shift = 4;   // 16 lanes: 128 columns
+    while (shift < 8 && (8 << shift) < K) ++shift;
+    const long long groups = (M + (kGatedThreads >> shift) - 1LL) / (kGatedThreads >> shift);
+    GatedArgs a{x, y_out, (uint8_t*)q, scales, ldx, x_dtype, y_dtype, M, K, (int)chunks, shift};
+    const bool nt = (size_t)M * K >= kStreamElements;
     w4h::begin_launches();
-    hipLaunchKernelGGL(silu_mul_quant_kernel, dim3((unsigned)(chunks * M)), dim3(kGatedThreads), 0,
-                       (hipStream_t)stream, a);
+    hipLaunchKernelGGL((nt ? silu_mul_quant_kernel<true> : silu_mul_quant_kernel<false>), dim3((unsigned)(chunks * groups)),
+                       dim3(kGatedThreads), 0, (hipStream_t)stream, a);
     w4h::set_last_variant("w8a8_silu_mul chunks=%lld rows=%d", chunks, M);
     return w4h::launch_status();
 }
