@@ -721,7 +721,7 @@ extern "C" int tree_attn(const void* q, long long q_stride, const void* k, const
     const long long blocks = (p.units * p.S + 7) / 8 * 8 * p.RB;
     const int R = T * (Hq / Hkv);
     const long long rows = p.units * R;
-    if (blocks > 0x7fffffffLL) return W4A16_ERR_UNSUPPORTED;
+    if (blocks * p.threads > kMaxLanes || (p.S > 1 && rows * kMergeWaves * 64 > kMaxLanes)) return W4A16_ERR_UNSUPPORTED;
     if (p.ws && !workspace) return W4A16_ERR_NULL;
     if (workspace_bytes < p.ws) return W4A16_ERR_WORKSPACE;
     int shift = 0;

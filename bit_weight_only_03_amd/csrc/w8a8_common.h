@@ -104,3 +104,5 @@ __device__ __forceinline__ void store_q8(uint8_t* p, const float* n, float s) {
 }
 
 }  // namespace w4k
+
+constexpr long long kMaxLanes = 0xffffffffLL;   // work-items of a launch

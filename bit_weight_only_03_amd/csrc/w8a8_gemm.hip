@@ -131,7 +131,7 @@ __device__ __forceinline__ bool merge_slices(const GemmArgs& a, int tile, int sl
 constexpr int kTableFloats = 2048;   // products of scales a workgroup holds
 
 template <int MT, int XR, int NT, int RD, int W>
-__global__ __launch_bounds__(W * 64) void w8a8_skinny_kernel(GemmArgs a) {
+__global__ __launch_bounds__(W * 64, 2) void w8a8_skinny_kernel(GemmArgs a) {
     constexpr int kSlot = (16 * NT + XR) * kStepK;
     constexpr int kLoads = 2 * NT + XR / 8;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(W * 64) void w8a8_skinny_kernel(GemmArgs a) {
 // consecutive columns of one row of y, stored 16 bytes at a time.  The key of
 // such a row follows r & 7, as its 8 neighbouring lanes need.
 template <int BM, int BN, int WGM, int WGN, int XD>
-__global__ __launch_bounds__(WGM * WGN * 64) void w8a8_tiled_kernel(GemmArgs a) {
+__global__ __launch_bounds__(WGM * WGN * 64, 2) void w8a8_tiled_kernel(GemmArgs a) {
     constexpr int W = WGM * WGN, WM = BM / WGM, WN = BN / WGN, MT = WM / 16, NT = WN / 16;
     constexpr int kXBuf = BM * kStepK, kWBuf = BN * kStepK;
     constexpr int XL = BM / (8 * W), WL = BN / (8 * W);   // loads per wave and step
@@ -592,7 +592,7 @@ extern "C" int w8a8_gemm(const void* x, const float* x_scales, const void* w, co
         !w4h::aligned16(w_scales) || !w4h::aligned16(y) || !w4h::aligned16(workspace))
         return W4A16_ERR_ALIGN;
     const Plan p = make_plan(M, N, K);
-    if (p.blocks > 0x7fffffffLL) return W4A16_ERR_UNSUPPORTED;
+    if (p.blocks * p.threads > kMaxLanes) return W4A16_ERR_UNSUPPORTED;
     if (p.ws && !workspace) return W4A16_ERR_NULL;
     if (workspace_bytes < p.ws) return W4A16_ERR_WORKSPACE;
     GemmArgs a{(const uint8_t*)x, x_scales, (const uint8_t*)w, w_scales, y,

@@ -205,6 +205,7 @@ extern "C" int w8a8_rmsnorm_quant(const void* x, int x_dtype, long long ldx, con
     const bool nt = (size_t)M * K >= kStreamElements;
     const int P = nv <= kMaxThreads ? 1 : nv <= 2 * kMaxThreads ? 2 : 4;
     const int threads = (((nv + P - 1) / P) + 63) / 64 * 64;
+    if ((long long)M * threads > kMaxLanes) return W4A16_ERR_UNSUPPORTED;
     auto kernel = P == 1   ? (nt ? rmsnorm_quant_kernel<1, true> : rmsnorm_quant_kernel<1, false>)
                   : P == 2 ? (nt ? rmsnorm_quant_kernel<2, true> : rmsnorm_quant_kernel<2, false>)
                            : (nt ? rmsnorm_quant_kernel<4, true> : rmsnorm_quant_kernel<4, false>);
@@ -229,6 +230,7 @@ extern "C" int w8a8_silu_mul_quant(const void* x, int x_dtype, long long ldx, vo
     const long long groups = (M + (kGatedThreads >> shift) - 1LL) / (kGatedThreads >> shift);
     GatedArgs a{x, y_out, (uint8_t*)q, scales, ldx, x_dtype, y_dtype, M, K, (int)chunks, shift};
     const bool nt = (size_t)M * K >= kStreamElements;
+    if (chunks * groups * kGatedThreads > kMaxLanes) return W4A16_ERR_UNSUPPORTED;
     w4h::begin_launches();
     hipLaunchKernelGGL((nt ? silu_mul_quant_kernel<true> : silu_mul_quant_kernel<false>), dim3((unsigned)(chunks * groups)),
                        dim3(kGatedThreads), 0, (hipStream_t)stream, a);
