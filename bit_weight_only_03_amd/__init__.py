@@ -115,11 +115,7 @@ EXPORTED_TREE = tuple(_SIGS_TREE)
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 _raw_stream = None
@@ -142,7 +138,7 @@ def _current_stream():
 
 def _stream(stream):
     if stream is None:
-        return _current_stream()
+        return (_raw_stream or _current_stream)()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -323,18 +319,28 @@ def w4a16_bw_probe(buf, nbytes: int, sink, stream=None):
     _check("w4a16_bw_probe", _lib.w4a16_bw_probe(_ptr(buf), nbytes, _ptr(sink), _stream(stream)))
 
 
+# The 8-bit layer's and the attention's calls are short on the device: dtypes go
+# through one lookup (numbers and unknown names as they are, for the library to refuse) and a
+# status of 0 through no call.
+_dt_of = {**_DTYPES, **{v: v for v in _DTYPES.values()}}.get
+
+
 def w8a8_rmsnorm_quant(x, x_dtype, ldx, residual, residual_dtype, h_out, weight, weight_dtype, eps,
                        y_out, y_dtype, q, scales, M, K, stream=None):
-    _check("w8a8_rmsnorm_quant", _lib.w8a8_rmsnorm_quant(
-        _ptr(x), _dt(x_dtype), ldx, _ptr(residual), _dt(residual_dtype), _ptr(h_out), _ptr(weight),
-        _dt(weight_dtype), eps, _ptr(y_out), _dt(y_dtype), _ptr(q), _ptr(scales), M, K,
-        _stream(stream)))
+    rc = _lib.w8a8_rmsnorm_quant(
+        _ptr(x), _dt_of(x_dtype, x_dtype), ldx, _ptr(residual), _dt_of(residual_dtype, residual_dtype),
+        _ptr(h_out), _ptr(weight), _dt_of(weight_dtype, weight_dtype), eps, _ptr(y_out),
+        _dt_of(y_dtype, y_dtype), _ptr(q), _ptr(scales), M, K, _stream(stream))
+    if rc:
+        _check("w8a8_rmsnorm_quant", rc)
 
 
 def w8a8_silu_mul_quant(x, x_dtype, ldx, y_out, y_dtype, q, scales, M, K, stream=None):
-    _check("w8a8_silu_mul_quant", _lib.w8a8_silu_mul_quant(
-        _ptr(x), _dt(x_dtype), ldx, _ptr(y_out), _dt(y_dtype), _ptr(q), _ptr(scales), M, K,
-        _stream(stream)))
+    rc = _lib.w8a8_silu_mul_quant(
+        _ptr(x), _dt_of(x_dtype, x_dtype), ldx, _ptr(y_out), _dt_of(y_dtype, y_dtype), _ptr(q),
+        _ptr(scales), M, K, _stream(stream))
+    if rc:
+        _check("w8a8_silu_mul_quant", rc)
 
 
 def w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -345,9 +351,11 @@ def w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
 
 def w8a8_gemm(x, x_scales, w, w_scales, y, y_dtype, M, N, K, workspace=None, workspace_bytes=0,
               stream=None):
-    _check("w8a8_gemm", _lib.w8a8_gemm(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(y),
-                                       _dt(y_dtype), M, N, K, _ptr(workspace), workspace_bytes,
-                                       _stream(stream)))
+    rc = _lib.w8a8_gemm(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(y),
+                        _dt_of(y_dtype, y_dtype), M, N, K, _ptr(workspace), workspace_bytes,
+                        _stream(stream))
+    if rc:
+        _check("w8a8_gemm", rc)
 
 
 def tree_attn_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
@@ -360,8 +368,10 @@ def tree_attn_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, max_len
 def tree_attn(q, q_stride, k, v, dtype, num_pages, page_size, page_stride, token_stride, head_stride,
               block_table, table_stride, lens, max_len, tree_mask, scale, out, lse, B, T, Hq, Hkv, D,
               workspace=None, workspace_bytes=0, stream=None):
-    _check("tree_attn", _lib.tree_attn(
-        _ptr(q), q_stride, _ptr(k), _ptr(v), _dt(dtype), num_pages, page_size, page_stride,
+    rc = _lib.tree_attn(
+        _ptr(q), q_stride, _ptr(k), _ptr(v), _dt_of(dtype, dtype), num_pages, page_size, page_stride,
         token_stride, head_stride, _ptr(block_table), table_stride, _ptr(lens), max_len,
         _ptr(tree_mask), scale, _ptr(out), _ptr(lse), B, T, Hq, Hkv, D, _ptr(workspace),
-        workspace_bytes, _stream(stream)))
+        workspace_bytes, _stream(stream))
+    if rc:
+        _check("tree_attn", rc)

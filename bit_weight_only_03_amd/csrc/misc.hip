@@ -17,9 +17,14 @@ constexpr int kProbeBlocks = 4096;
 constexpr int kProbeThreads = 256;
 
 constexpr int kMaxDevices = 64;
+constexpr int kNotedArgs = 8;
 std::atomic<int> g_cu_count[kMaxDevices];   // 0 = not queried yet
 
 thread_local char g_last_variant[160] = "none";
+// A variant noted by note_last_variant, written out when it is asked for.
+thread_local const char* g_noted = nullptr;
+thread_local const char* g_noted_name = nullptr;
+thread_local long long g_noted_args[kNotedArgs];
 thread_local char g_last_error[96] = "none";
 
 // Streams `n16` 16-byte words with non-temporal loads and folds them with
@@ -106,11 +111,24 @@ void set_last_variant(const char* fmt, ...) {
     va_start(ap, fmt);
     vsnprintf(g_last_variant, sizeof g_last_variant, fmt, ap);
     va_end(ap);
+    g_noted = nullptr;
+}
+void note_last_variant(const char* fmt, const char* name, const long long* args, int n) {
+    g_noted = fmt, g_noted_name = name;
+    for (int i = 0; i < kNotedArgs; ++i) g_noted_args[i] = i < n ? args[i] : 0;
 }
 void set_last_error(const char* what) { snprintf(g_last_error, sizeof g_last_error, "%s", what); }
 }  // namespace w4h
 
-extern "C" const char* w4a16_last_variant(void) { return g_last_variant; }
+extern "C" const char* w4a16_last_variant(void) {
+    if (g_noted) {
+        const long long* const a = g_noted_args;
+        snprintf(g_last_variant, sizeof g_last_variant, g_noted, g_noted_name, a[0], a[1], a[2], a[3], a[4], a[5], a[6],
+                 a[7]);
+        g_noted = nullptr;
+    }
+    return g_last_variant;
+}
 
 extern "C" const char* w4a16_last_error(void) { return g_last_error; }
 

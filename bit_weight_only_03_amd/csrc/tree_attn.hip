@@ -746,7 +746,7 @@ extern "C" int tree_attn(const void* q, long long q_stride, const void* k, const
                                           : (bf16 ? tree_merge_kernel<true, 256> : tree_merge_kernel<false, 256>);
         hipLaunchKernelGGL(merge, dim3((unsigned)rows), dim3(kMergeWaves * 64), 0, (hipStream_t)stream, a);
     }
-    w4h::set_last_variant("tree_attn D=%d rows=%d groups=%d threads=%d blocks=%lld splits=%d row_blocks=%d lds=%zu", D,
-                          p.rows, p.wk, p.threads, blocks, p.S, p.RB, p.lds);
+    w4h::note_variant("%s D=%lld rows=%lld groups=%lld threads=%lld blocks=%lld splits=%lld row_blocks=%lld lds=%lld",
+                      "tree_attn", D, p.rows, p.wk, p.threads, blocks, p.S, p.RB, p.lds);
     return w4h::launch_status();
 }

@@ -601,7 +601,7 @@ extern "C" int w8a8_gemm(const void* x, const float* x_scales, const void* w, co
     allow_lds();
     w4h::begin_launches();
     hipLaunchKernelGGL(p.kernel, dim3((unsigned)p.blocks), dim3(p.threads), p.lds, (hipStream_t)stream, a);
-    w4h::set_last_variant("w8a8_gemm %s tiles=%lldx%lld slices=%d threads=%d lds=%zu", p.name, p.tiles_m,
-                          p.tiles_n, p.S, p.threads, p.lds);
+    w4h::note_variant("w8a8_gemm %s tiles=%lldx%lld slices=%lld threads=%lld lds=%lld", p.name, p.tiles_m, p.tiles_n, p.S,
+                      p.threads, p.lds);
     return w4h::launch_status();
 }

@@ -211,7 +211,7 @@ extern "C" int w8a8_rmsnorm_quant(const void* x, int x_dtype, long long ldx, con
                            : (nt ? rmsnorm_quant_kernel<4, true> : rmsnorm_quant_kernel<4, false>);
     w4h::begin_launches();
     hipLaunchKernelGGL(kernel, dim3(M), dim3(threads), 0, (hipStream_t)stream, a);
-    w4h::set_last_variant("w8a8_rmsnorm passes=%d threads=%d rows=%d", P, threads, M);
+    w4h::note_variant("w8a8_%s passes=%lld threads=%lld rows=%lld", "rmsnorm", P, threads, M);
     return w4h::launch_status();
 }
 
@@ -234,6 +234,6 @@ extern "C" int w8a8_silu_mul_quant(const void* x, int x_dtype, long long ldx, vo
     w4h::begin_launches();
     hipLaunchKernelGGL((nt ? silu_mul_quant_kernel<true> : silu_mul_quant_kernel<false>), dim3((unsigned)(chunks * groups)),
                        dim3(kGatedThreads), 0, (hipStream_t)stream, a);
-    w4h::set_last_variant("w8a8_silu_mul chunks=%lld rows=%d", chunks, M);
+    w4h::note_variant("w8a8_%s chunks=%lld rows=%lld", "silu_mul", chunks, M);
     return w4h::launch_status();
 }
