@@ -319,25 +319,29 @@ def w4a16_bw_probe(buf, nbytes: int, sink, stream=None):
     _check("w4a16_bw_probe", _lib.w4a16_bw_probe(_ptr(buf), nbytes, _ptr(sink), _stream(stream)))
 
 
-# The 8-bit layer's and the attention's calls are short on the device: dtypes go
-# through one lookup (numbers and unknown names as they are, for the library to refuse) and a
-# status of 0 through no call.
-_dt_of = {**_DTYPES, **{v: v for v in _DTYPES.values()}}.get
+# The 8-bit layer's and the attention's calls are short on the device: a known dtype goes
+# through one lookup, and a status of 0 through no call.
+class _KnownDtypes(dict):
+    def __missing__(self, d):
+        return _dt(d)
+
+
+_dt_of = _KnownDtypes({**_DTYPES, **{v: v for v in _DTYPES.values()}})
 
 
 def w8a8_rmsnorm_quant(x, x_dtype, ldx, residual, residual_dtype, h_out, weight, weight_dtype, eps,
                        y_out, y_dtype, q, scales, M, K, stream=None):
     rc = _lib.w8a8_rmsnorm_quant(
-        _ptr(x), _dt_of(x_dtype, x_dtype), ldx, _ptr(residual), _dt_of(residual_dtype, residual_dtype),
-        _ptr(h_out), _ptr(weight), _dt_of(weight_dtype, weight_dtype), eps, _ptr(y_out),
-        _dt_of(y_dtype, y_dtype), _ptr(q), _ptr(scales), M, K, _stream(stream))
+        _ptr(x), _dt_of[x_dtype], ldx, _ptr(residual), _dt_of[residual_dtype],
+        _ptr(h_out), _ptr(weight), _dt_of[weight_dtype], eps, _ptr(y_out),
+        _dt_of[y_dtype], _ptr(q), _ptr(scales), M, K, _stream(stream))
     if rc:
         _check("w8a8_rmsnorm_quant", rc)
 
 
 def w8a8_silu_mul_quant(x, x_dtype, ldx, y_out, y_dtype, q, scales, M, K, stream=None):
     rc = _lib.w8a8_silu_mul_quant(
-        _ptr(x), _dt_of(x_dtype, x_dtype), ldx, _ptr(y_out), _dt_of(y_dtype, y_dtype), _ptr(q),
+        _ptr(x), _dt_of[x_dtype], ldx, _ptr(y_out), _dt_of[y_dtype], _ptr(q),
         _ptr(scales), M, K, _stream(stream))
     if rc:
         _check("w8a8_silu_mul_quant", rc)
@@ -352,7 +356,7 @@ def w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
 def w8a8_gemm(x, x_scales, w, w_scales, y, y_dtype, M, N, K, workspace=None, workspace_bytes=0,
               stream=None):
     rc = _lib.w8a8_gemm(_ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales), _ptr(y),
-                        _dt_of(y_dtype, y_dtype), M, N, K, _ptr(workspace), workspace_bytes,
+                        _dt_of[y_dtype], M, N, K, _ptr(workspace), workspace_bytes,
                         _stream(stream))
     if rc:
         _check("w8a8_gemm", rc)
@@ -369,7 +373,7 @@ def tree_attn(q, q_stride, k, v, dtype, num_pages, page_size, page_stride, token
               block_table, table_stride, lens, max_len, tree_mask, scale, out, lse, B, T, Hq, Hkv, D,
               workspace=None, workspace_bytes=0, stream=None):
     rc = _lib.tree_attn(
-        _ptr(q), q_stride, _ptr(k), _ptr(v), _dt_of(dtype, dtype), num_pages, page_size, page_stride,
+        _ptr(q), q_stride, _ptr(k), _ptr(v), _dt_of[dtype], num_pages, page_size, page_stride,
         token_stride, head_stride, _ptr(block_table), table_stride, _ptr(lens), max_len,
         _ptr(tree_mask), scale, _ptr(out), _ptr(lse), B, T, Hq, Hkv, D, _ptr(workspace),
         workspace_bytes, _stream(stream))
