@@ -354,3 +354,28 @@ def test_gemm_on_another_stream():
         y = run_gemm(*d)
     s.synchronize()
     assert same_bits(y, want)
+
+
+# Every kernel with K whole and in slices, at sizes that end inside its tiles.
+@pytest.mark.parametrize("M,N,K,kernel,split", [
+    (1, 72, 272, "skinny8x16", False), (5, 136, 8208, "skinny8x16", True),
+    (1, 10248, 144, "skinny8x32", False), (5, 2056, 17424, "skinny8x32", True),
+    (260, 136, 1040, "skinny16x32", False), (130, 136, 8208, "skinny16x32", True),
+    (600, 136, 3088, "skinny32x32", False), (65, 1032, 17424, "skinny32x32", True),
+    (65, 10248, 1040, "tiled64x128", False), (130, 4104, 5136, "tiled64x128", True),
+    (200, 10248, 1040, "tiled128x128", False), (65, 4104, 8208, "tiled128x128", True),
+    (200, 17416, 656, "tiled128x256", False), (500, 2056, 17424, "tiled128x256", True),
+    (2049, 4104, 144, "tiled256x256", False), (500, 4104, 17424, "tiled256x256", True),
+])
+def test_gemm_each_kernel_is_exact_on_integers(M, N, K, kernel, split):
+    # Products of at most 4 x 17424 terms times powers of two: exact in fp32 and in float64.
+    g = torch.Generator(device=DEV).manual_seed(M + N + K)
+    ints = lambda r, c, lo, hi: torch.randint(lo, hi, (r, c), generator=g, device=DEV)
+    x, w = (ints(r, K, -2, 3).float().to(FP8) for r in (M, N))
+    xs, ws = 2.0 ** ints(nblocks(K), M, -1, 2).float(), 2.0 ** ints(nblocks(N), nblocks(K), -1, 2).float()
+    y = run_gemm(x, xs, w, ws)
+    ran = L.w4a16_last_variant().split()
+    assert ran[1] == kernel and (ran[3] != "slices=1") == split, ran
+    x64 = x.double() * xs.double().t().repeat_interleave(128, 1)[:, :K]
+    w64 = w.double() * ws.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    assert torch.equal(y.double(), x64 @ w64.t())
