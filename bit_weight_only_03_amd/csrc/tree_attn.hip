@@ -143,6 +143,18 @@ __device__ __forceinline__ size_t out_row(const TreeArgs& a, uint32_t b, uint32_
     return ((size_t)b * a.T + row / G) * a.Hq + kvh * G + row % G;
 }
 
+// Scores, maxima, sums and O are fp32.  The probabilities are rounded to the
+// type of q, k and v, as the matrix unit takes them (the sum l adds them
+// before that): one rounding of 2^-9 (bf16) or 2^-12 (f16) per key, averaged over
+// the keys.
+//
+// One token over 150000 keys (614 MB of cache) takes 104 us, 5.9 TB/s: bound by
+// memory, two workgroups of four key groups per CU.  Four requests of 16 drafts
+// over up to 4097 keys (54 MB, 80 rows a kv head) take 26 us and the merge 5:
+// there a CU has one workgroup of four waves, each step (1.3 us) is a chain of
+// LDS reads, scores, maxima, exponentials and the product with V that nothing
+// overlaps.  Eight ring stages, eight waves in two key groups, non-temporal
+// loads and other page sizes were no faster there; deeper splits pay for their parts.
 template <bool BF16, int D, int RT, int WK, int WR, int NS>
 __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
     constexpr int DT = D / 16;                 // operand tiles of O^T
@@ -518,7 +530,10 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
 // Joins the S parts of each row: o = sum 2^(m_s - top) o_s / sum 2^(m_s - top) l_s.
 // A workgroup per row: wave w adds parts w, w + 4, .. in that order (all loads
 // of eight parts under way at once), then the four sums are added in wave
-// order.  Bound by latency: a row's parts are a few KiB.
+// order.  Bound by latency: a row's parts are a few KiB (2560 rows of 8 parts:
+// 5.4 us; a wave per row took longer, one workgroup waited for its parts in turn).  A launch of
+// its own, because the last workgroup of a unit would join 80 rows of 8 parts,
+// 330 KB, on one CU: 7 us at what a CU reads.
 constexpr int kMergeWaves = 4;
 template <bool BF16, int D>
 __global__ __launch_bounds__(kMergeWaves * 64) void tree_merge_kernel(TreeArgs a) {
@@ -711,7 +726,8 @@ extern "C" int tree_attn(const void* q, long long q_stride, const void* k, const
         (long long)table_stride * page_size < (long long)max_len + T)
         return W4A16_ERR_SHAPE;
     if (q_stride < (long long)Hq * D || q_stride % 8 || page_stride < 0 || token_stride < 0 || head_stride < 0 ||
-        (unsigned long long)page_size * (unsigned long long)token_stride >= (1ull << 30) || page_stride % 8 || token_stride % 8 || head_stride % 8 || !(scale == scale) || scale - scale != 0.f)
+        (unsigned long long)page_size * (unsigned long long)token_stride >= (1ull << 30) || page_stride % 8 ||
+        token_stride % 8 || head_stride % 8 || !(scale == scale) || scale - scale != 0.f)
         return W4A16_ERR_SHAPE;
     if (!w4h::aligned16(q) || !w4h::aligned16(k) || !w4h::aligned16(v) || !w4h::aligned16(out) ||
         !w4h::aligned16(workspace) || ((uintptr_t)lens & 3) || ((uintptr_t)block_table & 3) ||

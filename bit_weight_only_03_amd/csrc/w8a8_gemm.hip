@@ -17,6 +17,11 @@
 // Lane l of an operand holds row l & 15 and the chunks l >> 4 and 4 + (l >> 4)
 // of its 128 bytes.  Which k an MFMA slot stands for does not matter as long as
 // both operands agree.
+//
+// Roundings: the matrix unit aligns the products of 8 consecutive k to their
+// largest and drops what lies below 2^-13 of it (measured: rms 2e-6 of
+// sum |x w|); everything from the block's sum on is fp32, rounded once to y's
+// type.
 #include <math.h>
 
 #include <atomic>
@@ -86,8 +91,9 @@ __device__ __forceinline__ void store4(const GemmArgs& a, int m, int n, const fl
 // The merge of K slices inside the launch.  Of every slice's workgroup the
 // first `threads` threads hold C partial sums each.  They store them
 // (coherently across the device, thread-contiguous); the workgroup
-// counts itself in, and the last to arrive adds all slices in slice order: the result does not depend on who was last.  True for that workgroup, whose
-// f then holds the sums.  No workgroup waits for another.
+// counts itself in, and the last to arrive adds all slices in slice order: the
+// result does not depend on who was last.  True for that workgroup, whose f
+// then holds the sums.  No workgroup waits for another.
 template <int C>
 __device__ __forceinline__ bool merge_slices(const GemmArgs& a, int tile, int slice, int threads, bool live,
                                              unsigned* arrived, float* f) {
@@ -128,6 +134,13 @@ __device__ __forceinline__ bool merge_slices(const GemmArgs& a, int tile, int sl
 // bytes) that it fills RD units ahead and waits on alone: no barrier until the
 // waves' sums are added at the end.  MT tiles of 16 rows of x (XR = 8: half a
 // tile, whose other half repeats it and is not stored).
+//
+// Four waves per workgroup and two workgroups per CU keep about 100 KB of w on
+// its way to each CU.  1 x 34816 x 5120 takes 32 us (5.6 TB/s of w), 32 rows of it
+// 42, 1 x 7168 x 5120 9 us (4 TB/s: about 5 us are a launch's start, its first
+// loads and its last sum).  K slices pay only where tiles leave most CUs idle:
+// 64 x 7168 x 5120 takes 16.6 us whole, 22 and 30 in two and four slices.
+// Starting each tile at another k (other memory channels at one time) changed nothing.
 constexpr int kTableFloats = 2048;   // products of scales a workgroup holds
 
 template <int MT, int XR, int NT, int RD, int W>
@@ -267,8 +280,17 @@ __global__ __launch_bounds__(W * 64, 2) void w8a8_skinny_kernel(GemmArgs a) {
 // ---- many rows ----
 //
 // Bound by the matrix units.  A workgroup of WGM x WGN waves takes BM rows of x
-// by BN rows of w; each step's 128 k of both go to one of two LDS buffers while
-// the other is multiplied, one barrier per step.
+// by BN rows of w; each step's 128 k go to LDS rings, x's of XD blocks and w's of
+// three, while an older block is multiplied: one barrier per step.
+//
+// 8192 x 8192 x 8192 takes 454 us (2.42 PFLOP/s; the library's product with one
+// scale for all of x and w reaches 2.6), 4096 x 34816 x 5120 650 to 680 (2.14 to
+// 2.24: its 2176 tiles are 8.5 rounds of 256 CUs).  A step of the largest tile is
+// 32 MFMAs of 32 clocks for each of a SIMD's two waves, and beside them 24 LDS
+// reads and 128 fmas per wave; these run under products only if a wave never
+// waits for the product it has just asked for: hence kLag.  At 64 to 128 rows
+// w's stream bounds it (128 x 34816 x 5120: 59 us, 3 TB/s of w); tiles of 64 x 64
+// and 128 x 64 and deeper rings of x were within 5 percent there.
 //
 // Inside a wave's WN columns, row r of operand tile t is column
 // (r >> 2) WN/4 + 4 t + (r & 3): a lane's results over all tiles are then WN/4
@@ -280,7 +302,7 @@ __global__ __launch_bounds__(WGM * WGN * 64, 2) void w8a8_tiled_kernel(GemmArgs 
     constexpr int kXBuf = BM * kStepK, kWBuf = BN * kStepK;
     constexpr int XL = BM / (8 * W), WL = BN / (8 * W);   // loads per wave and step
     constexpr int kAll = XL + WL;
-    constexpr int kLag = 3;   // products under way between one and its scaling (1: 691, 2: 678, 3: 665, 4: 672 us)
+    constexpr int kLag = 3;   // products under way between one and its scaling (4096 x 34816 x 5120 with 1: 691, 2: 678, 3: 665, 4: 672 us)
     static_assert(XL >= 1 && WL >= 1 && WN <= 128 && WN >= 32, "tile shape");
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
