@@ -6,6 +6,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 
 import pytest
 
@@ -100,3 +101,15 @@ def test_gemm_refusals_and_sizes():
         for N in (8, 512, 5120, 34816):
             for K in (16, 128, 5136, 17408, 1 << 20):
                 assert lib.w8a8_workspace_bytes(M, N, K) <= lib.W4A16_WORKSPACE_HEAD_BYTES + (64 << 20)
+
+
+def test_gemm_refuses_overridden_slices_that_leave_no_plan():
+    # 8 slices of 4096 x 34816 in 256 x 256 tiles need more than the largest workspace: no kernel may be launched.
+    code = ("import ctypes, bit_weight_only_03_amd as L\n"
+            "lib = ctypes.CDLL(L.LIB_PATH)\n"
+            "p = ctypes.c_void_p(4096)\n"
+            "print(lib.w8a8_gemm(p, p, p, p, p, 1, 4096, 34816, 5120, p, ctypes.c_size_t(1 << 40), None))\n")
+    env = dict(os.environ, W8A8_VARIANT="7", W8A8_SPLIT="8")
+    out = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert out.returncode == 0, out.stderr[-500:]
+    assert int(out.stdout.split()[-1]) == -6   # W4A16_ERR_UNSUPPORTED
