@@ -547,8 +547,8 @@ Plan make_plan(int M, int N, int K) {
         const Kernel& k = kKernels[v];
         if (only >= 0 && only < kKernelCount ? v != only : (M < k.from || M > k.to)) continue;
         Plan p = k.p;
-        p.tiles_m = (M + p.bm - 1) / p.bm;
-        p.tiles_n = (N + p.bn - 1) / p.bn;
+        p.tiles_m = ((long long)M + p.bm - 1) / p.bm;
+        p.tiles_n = ((long long)N + p.bn - 1) / p.bn;   // N + bn - 1 may pass 32 bits
         const long long all = p.tiles_m * p.tiles_n;
         const int tiles = all < (1 << 24) ? (int)all : 1 << 24;   // more never has slices
         const int waves = k.skinny ? p.threads / 64 : 1;          // units a step takes

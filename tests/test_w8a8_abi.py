@@ -113,3 +113,27 @@ def test_gemm_refuses_overridden_slices_that_leave_no_plan():
     out = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert out.returncode == 0, out.stderr[-500:]
     assert int(out.stdout.split()[-1]) == -6   # W4A16_ERR_UNSUPPORTED
+
+
+def gemm_statuses_without_a_device(*shapes):
+    """(size query's status, call's status) of each M, N, K in a process that sees no GPU: a call that passes the
+    checks reports its failed launch (W4A16_ERR_HIP), nothing runs."""
+    code = ("import ctypes, sys, bit_weight_only_03_amd as L\n"
+            "lib = ctypes.CDLL(L.LIB_PATH)\n"
+            "p, b = ctypes.c_void_p(4096), ctypes.c_size_t()\n"
+            "for s in sys.argv[1:]:\n"
+            "    M, N, K = (int(v) for v in s.split('x'))\n"
+            "    q = lib.w8a8_workspace_bytes(M, N, K, ctypes.byref(b))\n"
+            "    print(q, lib.w8a8_gemm(p, p, p, p, p, 1, M, N, K, p, ctypes.c_size_t(1 << 40), None))\n")
+    env = {k: v for k, v in os.environ.items() if not k.startswith("W8A8_")}
+    out = subprocess.run([sys.executable, "-c", code, *("%dx%dx%d" % s for s in shapes)], env=dict(env, HIP_VISIBLE_DEVICES="-1"),
+                         capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert out.returncode == 0, out.stderr[-500:]
+    return [tuple(int(v) for v in line.split()) for line in out.stdout.split("\n")[-len(shapes) - 1:-1]]
+
+
+def test_gemm_counts_the_tiles_of_the_largest_n():
+    # N + 255 passes 32 bits: more workgroups than a launch takes, whatever the kernel, and so refused.
+    for (_, rc), M in zip(gemm_statuses_without_a_device((1, 2**31 - 8, 16), (8, 2**31 - 8, 16), (16, 2**31 - 8, 16), (600, 2**31 - 8, 16)),
+                          (1, 8, 16, 600)):
+        assert rc == -6, M   # W4A16_ERR_UNSUPPORTED
