@@ -538,14 +538,19 @@ constexpr int kKernelCount = sizeof kKernels / sizeof kKernels[0];
 // The kernel and the slices of K with the least estimated time: rounds of
 // workgroups over the CUs, each a start and its steps, not faster than w
 // arrives; slices add their partial sums' traffic and the merge.
+//
+// The kernels of few rows have to slice a sum whose scales pass their table
+// (K > 32768 up to 8 rows, 16384 up to 16): over very many columns those slices
+// pass the counters or the partial sums' limit.  Where the kernels meant for M leave
+// no plan like this, all are looked at: the tiled ones hold no table.  None is left
+// only past a launch's size (M N from about 2^39) or under overridden slices.
 Plan make_plan(int M, int N, int K) {
     const int kb = (K + kStepK - 1) / kStepK, cus = w4h::cu_count();
     const int only = w4h::overrides().w8_variant, slices = w4h::overrides().w8_split;
+    const bool any = only < 0 || only >= kKernelCount;
     Plan best{};
     float least = 0;
-    for (int v = 0; v < kKernelCount; ++v) {
-        const Kernel& k = kKernels[v];
-        if (only >= 0 && only < kKernelCount ? v != only : (M < k.from || M > k.to)) continue;
+    auto look_at = [&](const Kernel& k) {
         Plan p = k.p;
         p.tiles_m = ((long long)M + p.bm - 1) / p.bm;
         p.tiles_n = ((long long)N + p.bn - 1) / p.bn;   // N + bn - 1 may pass 32 bits
@@ -566,6 +571,8 @@ Plan make_plan(int M, int N, int K) {
             if (k.skinny && ((kb + S - 1) / S) * p.bm > kTableFloats) continue;
             const size_t partials = S > 1 ? (size_t)tiles * S * p.floats * sizeof(float) : 0;
             if (S > 1 && (tiles > kCounters || partials > kMaxPartials)) continue;
+            p.blocks = k.skinny ? (p.tiles_n * S + 7) / 8 * 8 * p.tiles_m : (all * S + 7) / 8 * 8;
+            if (p.blocks * p.threads > kMaxLanes) continue;
             const float wgs = (float)all * S, steps = (float)((kb + S * waves - 1) / (S * waves));
             float t = ceilf(wgs / slots) * (k.start + steps * (wgs > cus ? k.beside : k.alone));
             t = fmaxf(t, k.start + (float)N * K / k.stream);
@@ -575,10 +582,13 @@ Plan make_plan(int M, int N, int K) {
                 best = p;
                 best.S = S;
                 best.ws = w4h::ws_bytes(partials);
-                best.blocks = k.skinny ? (p.tiles_n * S + 7) / 8 * 8 * p.tiles_m : (all * S + 7) / 8 * 8;
             }
         }
-    }
+    };
+    for (int v = 0; v < kKernelCount; ++v)
+        if (any ? M >= kKernels[v].from && M <= kKernels[v].to : v == only) look_at(kKernels[v]);
+    if (any && !best.kernel)
+        for (const Kernel& k : kKernels) look_at(k);
     return best;
 }
 
@@ -603,7 +613,9 @@ int check_shape(int M, int N, int K) {
 extern "C" int w8a8_workspace_bytes(int M, int N, int K, size_t* bytes) {
     if (!bytes) return W4A16_ERR_NULL;
     if (int rc = check_shape(M, N, K)) return rc;
-    *bytes = make_plan(M, N, K).ws;
+    const Plan p = make_plan(M, N, K);
+    if (!p.kernel) return W4A16_ERR_UNSUPPORTED;
+    *bytes = p.ws;
     return W4A16_OK;
 }
 
@@ -617,8 +629,7 @@ extern "C" int w8a8_gemm(const void* x, const float* x_scales, const void* w, co
         !w4h::aligned16(w_scales) || !w4h::aligned16(y) || !w4h::aligned16(workspace))
         return W4A16_ERR_ALIGN;
     const Plan p = make_plan(M, N, K);
-    if (!p.kernel) return W4A16_ERR_UNSUPPORTED;   // only overridden slices leave no plan
-    if (p.blocks * p.threads > kMaxLanes) return W4A16_ERR_UNSUPPORTED;
+    if (!p.kernel) return W4A16_ERR_UNSUPPORTED;
     if (p.ws && !workspace) return W4A16_ERR_NULL;
     if (workspace_bytes < p.ws) return W4A16_ERR_WORKSPACE;
     GemmArgs a{(const uint8_t*)x, x_scales, (const uint8_t*)w, w_scales, y,

@@ -62,7 +62,9 @@ int w8a8_silu_mul_quant(const void* x, int x_dtype, long long ldx, void* y_out, 
  * y [M][N] contiguous, y_dtype f32, f16 or bf16 (rounded once).  Shape:
  * 1 <= M <= 2^26, N >= 8, N % 8 == 0, 16 <= K <= 2^20, K % 16 == 0.  M is not limited to a
  * few rows: one token to whole prompts.  x, w, y and the workspace do not overlap.
- * workspace may be NULL where w8a8_workspace_bytes reports 0. */
+ * workspace may be NULL where w8a8_workspace_bytes reports 0.  Both calls return
+ * W4A16_ERR_UNSUPPORTED where a product needs more work-items than a launch takes
+ * (2^32 - 1; M * N from about 2^39). */
 int w8a8_workspace_bytes(int M, int N, int K, size_t* bytes);
 int w8a8_gemm(const void* x, const float* x_scales, const void* w, const float* w_scales, void* y,
               int y_dtype, int M, int N, int K, void* workspace, size_t workspace_bytes,

@@ -379,3 +379,24 @@ def test_gemm_each_kernel_is_exact_on_integers(M, N, K, kernel, split):
     x64 = x.double() * xs.double().t().repeat_interleave(128, 1)[:, :K]
     w64 = w.double() * ws.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
     assert torch.equal(y.double(), x64 @ w64.t())
+
+
+def test_gemm_few_rows_of_a_long_sum_over_very_many_columns():
+    # 9 rows, K past what the few-row kernels' scales hold unsliced, more columns than slices have counters for: 8.6 GB
+    # of w.  Products of at most 4 x 16400 terms times powers of two: exact in fp32 and in float64.
+    M, N, K, rows = 9, 524296, 16400, 16384
+    g = torch.Generator(device=DEV).manual_seed(5)
+    codes = torch.tensor([-2, -1, 0, 1, 2], device=DEV, dtype=torch.float32).to(FP8).view(torch.uint8)
+    w = torch.empty(N, K, dtype=torch.uint8, device=DEV)
+    for n in range(0, N, rows):
+        w[n:n + rows] = codes[torch.randint(0, 5, w[n:n + rows].shape, generator=g, device=DEV, dtype=torch.int32)]
+    w = w.view(FP8)
+    x = torch.randint(-2, 3, (M, K), generator=g, device=DEV).float().to(FP8)
+    xs = 2.0 ** torch.randint(-1, 2, (nblocks(K), M), generator=g, device=DEV).float()
+    ws = 2.0 ** torch.randint(-1, 2, (nblocks(N), nblocks(K)), generator=g, device=DEV).float()
+    y = run_gemm(x, xs, w, ws)
+    x64 = x.double() * xs.double().t().repeat_interleave(128, 1)[:, :K]
+    for n in range(0, N, rows):
+        b = ws[n // 128:(n + rows) // 128].double()
+        w64 = w[n:n + rows].double() * b.repeat_interleave(128, 0)[:N - n].repeat_interleave(128, 1)[:, :K]
+        assert torch.equal(y[:, n:n + rows].double(), x64 @ w64.t()), n

@@ -137,3 +137,16 @@ def test_gemm_counts_the_tiles_of_the_largest_n():
     for (_, rc), M in zip(gemm_statuses_without_a_device((1, 2**31 - 8, 16), (8, 2**31 - 8, 16), (16, 2**31 - 8, 16), (600, 2**31 - 8, 16)),
                           (1, 8, 16, 600)):
         assert rc == -6, M   # W4A16_ERR_UNSUPPORTED
+
+
+def test_gemm_long_sums_over_many_columns_have_a_plan():
+    # Up to 16 rows, K past what the table of scales holds, and so many columns that the slices pass their limits: by the
+    # counters (the first two) and by the partial sums' size (the others).
+    shapes = [(9, 524296, 16400), (1, 524296, 32784), (16, 152064, 131072), (1, 34816, 1 << 20), (1, 65536, 1 << 20), (1, 1 << 30, 16)]
+    for got, s in zip(gemm_statuses_without_a_device(*shapes), shapes):
+        assert got == (0, -7), (s, got)   # as far as the launch: W4A16_ERR_HIP
+
+
+def test_gemm_size_query_refuses_what_the_call_refuses():
+    for got in gemm_statuses_without_a_device((1, 2**31 - 8, 16), (1 << 26, 1 << 14, 16)):
+        assert got == (-6, -6), got
