@@ -113,6 +113,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormArgs a) {
 // t = -g log2(e) is taken in two pieces, the rounding of the product and the
 // rest of the constant, so that 2^t keeps its relative error for large |g|.
 // exp(-g) past fp32's range is infinite and the result 0, as in the formula.
+// The reciprocal unit flushes a result below 2^-126 to zero, so it takes
+// (1 + p) / 16: 1 / (1 + p) is subnormal from g = -87.3 on, its product with g is not.
 __device__ __forceinline__ float silu(float g) {
     constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
     const float t = -g * kLog2e;
@@ -120,8 +122,8 @@ __device__ __forceinline__ float silu(float g) {
     float p = __builtin_amdgcn_exp2f(t);
     // Not where p is 0 or infinite: there the correction could be 0 * inf.
     const float c = p * (kLn2 * rest);
-    p = __builtin_fabsf(t) < 126.0f ? p + c : p;
-    return g * __builtin_amdgcn_rcpf(1.0f + p);
+    p = __builtin_fabsf(t) < 128.0f ? p + c : p;
+    return g * (__builtin_amdgcn_rcpf(__builtin_fmaf(p, 0x1p-4f, 0x1p-4f)) * 0x1p-4f);
 }
 
 struct GatedArgs {

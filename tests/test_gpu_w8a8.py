@@ -400,3 +400,16 @@ def test_gemm_few_rows_of_a_long_sum_over_very_many_columns():
         b = ws[n // 128:(n + rows) // 128].double()
         w64 = w[n:n + rows].double() * b.repeat_interleave(128, 0)[:N - n].repeat_interleave(128, 1)[:, :K]
         assert torch.equal(y[:, n:n + rows].double(), x64 @ w64.t()), n
+
+
+def test_gated_where_the_reciprocal_is_subnormal():
+    # g from -87.34 to -88.72: exp(-g) is within fp32's range and 1 / (1 + exp(-g)) below 2^-126, while the product with a
+    # large u is an ordinary number (1e-24).  The subnormal reciprocal has 21 bits at least: 2^-21 beside the 64 u.
+    K, n = 256, 200
+    gate = torch.zeros(1, K)
+    gate[0, :n] = torch.linspace(-87.0, -88.72, n)
+    x = torch.cat([gate, torch.full((1, K), 2.0 ** 40)], 1)
+    want = (gate.double() / (1 + torch.exp(-gate.double())) * 2.0 ** 40)[0, :n]
+    y = torch.empty(1, K, device=DEV)
+    L.w8a8_silu_mul_quant(x.to(DEV), "f32", 2 * K, y, "f32", None, None, 1, K)
+    assert torch.all((y.cpu().double()[0, :n] - want).abs() <= (64 * U + 2.0 ** -21) * want.abs())
