@@ -745,8 +745,9 @@ extern "C" int tree_attn(const void* q, long long q_stride, const void* k, const
     TreeArgs a{};
     a.q = (const uint16_t*)q, a.k = (const uint16_t*)k, a.v = (const uint16_t*)v;
     a.table = block_table, a.lens = lens, a.mask = tree_mask, a.out = out, a.lse = lse;
-    a.part_ml = (float2*)w4h::ws_part(workspace);
-    a.part_o = workspace ? (float*)(a.part_ml + (size_t)rows * p.S) : nullptr;
+    // The sums first: a multiple of 64 floats, so they and the pairs behind them are aligned for any number of rows and splits.
+    a.part_o = (float*)w4h::ws_part(workspace);
+    a.part_ml = workspace ? (float2*)(a.part_o + (size_t)rows * p.S * D) : nullptr;
     a.q_stride = q_stride, a.page_stride = page_stride, a.token_stride = token_stride, a.head_stride = head_stride;
     a.num_pages = num_pages, a.page_shift = shift, a.table_stride = table_stride, a.max_len = max_len;
     a.scale2 = fmaxf(fabsf(scale) * kLog2e, 0x1p-126f);   // not 0: -inf marks what a row does not see

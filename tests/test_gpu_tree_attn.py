@@ -337,3 +337,21 @@ def test_graph_replays_with_other_lengths_and_a_shared_workspace():
         assert torch.equal(outs[1][0].view(torch.int16), want[1][0].view(torch.int16))
     assert torch.equal(outs[0][0].view(torch.int16), want[0][0].view(torch.int16))
     assert not work[:L.W4A16_WORKSPACE_HEAD_BYTES].any()
+
+
+def test_parts_of_an_odd_number_of_rows_and_splits_are_aligned():
+    # The sums of the parts are stored 16 bytes at a time: they have to begin the scratch (16-byte aligned), the pairs
+    # (maximum in log2 units, sum) follow.  Joined from there they are the call's result.
+    c = Case(1, 1, 5, 1, 128, 16, "bf16", [1200])
+    need = L.tree_attn_workspace_bytes(1, 1, 5, 1, 128, 1200)
+    work = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    out, lse = c.run(work=work)
+    splits = int(dict(f.split("=") for f in L.w4a16_last_variant().split()[1:])["splits"])
+    assert splits > 1 and (5 * splits) % 2 == 1
+    parts = work[L.W4A16_WORKSPACE_HEAD_BYTES:].view(torch.float32)
+    o = parts[:5 * splits * 128].view(5, splits, 128).cpu().double()
+    m, l = parts[5 * splits * 128:][:5 * splits * 2].view(5, splits, 2).cpu().double().unbind(2)
+    f = torch.exp2(m - m.amax(1, keepdim=True))
+    want = (f[:, :, None] * o).sum(1) / (f * l).sum(1, keepdim=True)
+    assert torch.all((out.cpu().double()[0] - want).abs() <= UT["bf16"] * want.abs() + 64 * U * (f[:, :, None] * o).abs().sum(1) / (f * l).sum(1, keepdim=True))
+    c.check(out, lse)
