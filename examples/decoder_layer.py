@@ -24,6 +24,7 @@ if ROOT not in sys.path:
 
 import bit_weight_only_03_amd as L  # noqa: E402
 
+O_ROWS = 64     # rows the 4-bit product takes in a call
 FP8 = torch.float8_e4m3fn
 BF16 = torch.bfloat16
 
@@ -71,9 +72,14 @@ class Layer:
         self.gu, self.a8 = new(M, 2 * w.inner), new(M, w.inner, dtype=FP8)
         self.as_, self.y = new(blocks(w.inner), M, dtype=torch.float32), new(M, w.hidden)
         n = max(L.w8a8_workspace_bytes(M, self.qkv.shape[1], w.hidden), L.w8a8_workspace_bytes(M, 2 * w.inner, w.hidden),
-                L.w8a8_workspace_bytes(M, w.hidden, w.inner), L.w4a16_workspace_bytes(M, w.hidden, w.q_heads * w.D, 128),
+                L.w8a8_workspace_bytes(M, w.hidden, w.inner),
+                *(L.w4a16_workspace_bytes(m, w.hidden, w.q_heads * w.D, 128) for m in self.o_rows()),
                 L.tree_attn_workspace_bytes(B, T, w.q_heads, w.kv_heads, w.D, max_len))
         self.work = torch.zeros(max(n, 16), dtype=torch.uint8, device=dev)   # its head has to start as zeros
+
+    def o_rows(self):
+        """The rows of each call of the output projection."""
+        return [min(O_ROWS, self.M - m) for m in range(0, self.M, O_ROWS)]
 
     def product(self, x8, xs, weight, y):
         (q, s), (M, N) = weight, y.shape
@@ -93,7 +99,8 @@ class Layer:
         ps, ts, hs = self.k.stride()[:3]
         L.tree_attn(self.qkv, self.qkv.stride(0), self.k, self.v, "bf16", self.k.shape[0], self.page, ps, ts, hs, table, table.shape[1],
                     lens, self.max_len, mask, w.D ** -0.5, self.att, None, B, T, w.q_heads, w.kv_heads, w.D, self.work, self.work.numel())
-        L.w4a16_gemv(self.att, "bf16", *w.o, self.o, "bf16", M, w.hidden, qw, 128, self.work, self.work.numel())
+        for i, m in enumerate(self.o_rows()):
+            L.w4a16_gemv(self.att[O_ROWS * i:], "bf16", *w.o, self.o[O_ROWS * i:], "bf16", m, w.hidden, qw, 128, self.work, self.work.numel())
         L.w8a8_rmsnorm_quant(self.o, "bf16", w.hidden, x, "bf16", self.h, w.norm2, "bf16", 1e-6, None, "bf16", self.x8, self.xs, M, w.hidden)
         self.product(self.x8, self.xs, w.gate_up, self.gu)
         L.w8a8_silu_mul_quant(self.gu, "bf16", 2 * w.inner, None, "bf16", self.a8, self.as_, M, w.inner)

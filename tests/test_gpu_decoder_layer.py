@@ -104,3 +104,8 @@ def test_layer_matches_its_steps(B, T, lens):
     # The whole MLP from the 64-bit start.
     gate, up = gu.split(inner, 1)
     assert rel(y, e4m3(gate * torch.sigmoid(gate) * up) @ values(w.down).t()) < 2.0 ** -4
+
+
+@pytest.mark.parametrize("B,T,lens", [(5, 16, [300, 12, 0, 77, 41]), (2, 40, [130, 5])])
+def test_layer_with_more_rows_than_the_4_bit_product_takes_at_once(B, T, lens):
+    test_layer_matches_its_steps(B, T, lens)
