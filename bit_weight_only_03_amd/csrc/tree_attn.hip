@@ -600,6 +600,7 @@ struct Plan {
     size_t lds;
     int S, RB;
     long long units;      // requests x kv heads
+    long long blocks;
     size_t ws;
 };
 
@@ -642,6 +643,7 @@ const Shape* shapes(int D, int& n) { return D == 64 ? shapes<64>(n) : D == 128 ?
 // over many keys want many groups of keys, many rows a kernel whose waves share
 // the keys' tiles; a split fills the GPU but pays for its parts' traffic and the merge's
 // launch.  The estimate takes the longest request (max_len) for all of them.
+// No kernel is left where all need more work-items than a launch takes.
 Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_len) {
     constexpr double kStart = 7.0, kMerge = 5.0, kPartBytesPerUs = 4e6;   // launch to first tile and last store; merge
     const int R = T * (Hq / Hkv), cus = w4h::cu_count();
@@ -663,7 +665,8 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_len) {
             S = S < tiles / (2 * p.wk) ? S : tiles / (2 * p.wk);   // two tiles at least for each group
             S = S < 1 ? 1 : S;
             p.ws = S > 1 ? w4h::ws_bytes((size_t)units * R * S * (D + 2) * sizeof(float)) : 0;
-            if (p.ws > kMaxWorkspace) continue;
+            p.blocks = (units * S + 7) / 8 * 8 * p.RB;
+            if (p.ws > kMaxWorkspace || p.blocks * p.threads > kMaxLanes || (S > 1 && units * R * kMergeWaves * 64 > kMaxLanes)) continue;
             const double wgs = (double)units * p.RB * S, steps = ceil((double)tiles / S / p.wk);
             const double rounds = ceil(wgs / ((double)cus * occupancy));
             double t = rounds * (kStart + steps * (wgs > cus ? sh[i].beside : sh[i].alone));
@@ -709,7 +712,9 @@ int check_shape(int B, int T, int Hq, int Hkv, int D, int max_len) {
 extern "C" int tree_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int max_len, size_t* bytes) {
     if (!bytes) return W4A16_ERR_NULL;
     if (int rc = check_shape(B, T, Hq, Hkv, D, max_len)) return rc;
-    *bytes = make_plan(B, T, Hq, Hkv, D, max_len).ws;
+    const Plan p = make_plan(B, T, Hq, Hkv, D, max_len);
+    if (!p.rows) return W4A16_ERR_UNSUPPORTED;
+    *bytes = p.ws;
     return W4A16_OK;
 }
 
@@ -734,10 +739,9 @@ extern "C" int tree_attn(const void* q, long long q_stride, const void* k, const
         ((uintptr_t)tree_mask & 7) || ((uintptr_t)lse & 3))
         return W4A16_ERR_ALIGN;
     const Plan p = make_plan(B, T, Hq, Hkv, D, max_len);
-    const long long blocks = (p.units * p.S + 7) / 8 * 8 * p.RB;
+    if (!p.rows) return W4A16_ERR_UNSUPPORTED;
     const int R = T * (Hq / Hkv);
     const long long rows = p.units * R;
-    if (blocks * p.threads > kMaxLanes || (p.S > 1 && rows * kMergeWaves * 64 > kMaxLanes)) return W4A16_ERR_UNSUPPORTED;
     if (p.ws && !workspace) return W4A16_ERR_NULL;
     if (workspace_bytes < p.ws) return W4A16_ERR_WORKSPACE;
     int shift = 0;
@@ -756,7 +760,7 @@ extern "C" int tree_attn(const void* q, long long q_stride, const void* k, const
     const bool bf16 = dtype == W4A16_BF16;
     allow_lds();
     w4h::begin_launches();
-    hipLaunchKernelGGL(p.kernel[bf16], dim3((unsigned)blocks), dim3(p.threads), p.lds, (hipStream_t)stream, a);
+    hipLaunchKernelGGL(p.kernel[bf16], dim3((unsigned)p.blocks), dim3(p.threads), p.lds, (hipStream_t)stream, a);
     if (p.S > 1) {
         const kernel_t merge = D == 64    ? (bf16 ? tree_merge_kernel<true, 64> : tree_merge_kernel<false, 64>)
                                : D == 128 ? (bf16 ? tree_merge_kernel<true, 128> : tree_merge_kernel<false, 128>)
@@ -764,6 +768,6 @@ extern "C" int tree_attn(const void* q, long long q_stride, const void* k, const
         hipLaunchKernelGGL(merge, dim3((unsigned)rows), dim3(kMergeWaves * 64), 0, (hipStream_t)stream, a);
     }
     w4h::note_variant("%s D=%lld rows=%lld groups=%lld threads=%lld blocks=%lld splits=%lld row_blocks=%lld lds=%lld",
-                      "tree_attn", D, p.rows, p.wk, p.threads, blocks, p.S, p.RB, p.lds);
+                      "tree_attn", D, p.rows, p.wk, p.threads, p.blocks, p.S, p.RB, p.lds);
     return w4h::launch_status();
 }

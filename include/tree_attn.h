@@ -42,11 +42,13 @@ extern "C" {
  * out         [B*T][Hq][D], contiguous, of dtype; lse fp32 [B*T][Hq] or NULL
  * dtype       W4A16_F16 or W4A16_BF16, of q, k, v and out.  Products and sums
  *             are fp32; the probabilities take the dtype for the product with v.
- * Shape: B >= 1, 1 <= T <= 64, Hq a multiple of Hkv, D 64, 128 or 256,
- * page_size a power of two with page_size * token_stride < 2^30, 0 <= max_len <= 2^30, table_stride * page_size >=
+ * Shape: B >= 1, 1 <= T <= 64, Hq a multiple of Hkv, Hq <= 2^16, B * Hq <= 2^24, D 64, 128
+ * or 256, page_size a power of two with page_size * token_stride < 2^30, 0 <= max_len <= 2^30, table_stride * page_size >=
  * max_len + T.  max_len bounds lens (host knowledge: it sizes the split over the
  * keys; a captured graph stays valid for every lens up to it).  Deterministic
- * for the same lens.  workspace may be NULL where the query reports 0. */
+ * for the same lens.  workspace may be NULL where the query reports 0.  Both calls
+ * return W4A16_ERR_UNSUPPORTED for another D, and where a launch would need 2^32
+ * work-items (at the earliest with 2^24 pairs of a request and a kv head, or 2^28 rows B * T * Hq). */
 int tree_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int max_len, size_t* bytes);
 int tree_attn(const void* q, long long q_stride, const void* k, const void* v, int dtype,
               int num_pages, int page_size, long long page_stride, long long token_stride,

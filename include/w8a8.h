@@ -37,7 +37,9 @@ extern "C" {
  * residual may be NULL (h_out then has to be NULL too), h_out may be NULL or
  * the residual itself (updated in place); y_out or the pair q, scales may be NULL,
  * not both.  Otherwise nothing overlaps.  Shape: M >= 1, 16 <= K <= 32768,
- * K % 16 == 0; eps finite and >= 0.  A longer K returns W4A16_ERR_UNSUPPORTED.
+ * K % 16 == 0; eps finite and >= 0.  A longer K returns W4A16_ERR_UNSUPPORTED, and
+ * so does a launch of 2^32 work-items (a row takes one for each 8 columns up to 1024,
+ * 64 at least: M from 2^26 where K <= 512, at the earliest from 2^22).
  * A row with a NaN gives NaN throughout, one with an infinity NaN in its
  * block, as the formula does in fp32. */
 int w8a8_rmsnorm_quant(const void* x, int x_dtype, long long ldx, const void* residual,
@@ -48,7 +50,9 @@ int w8a8_rmsnorm_quant(const void* x, int x_dtype, long long ldx, const void* re
 /* n[m][k] = silu(x[m][k]) * x[m][K + k], silu(g) = g / (1 + exp(-g)), in fp32;
  * then q, scales and y_out as above.  x [M][2K] (the fused gate/up product)
  * with ldx elements from row to row (ldx >= 2K, a multiple of 8), x_dtype f16, bf16 or
- * f32.  Shape: M >= 1, K >= 16, K % 16 == 0. */
+ * f32.  Shape: M >= 1, 16 <= K <= 2^30, K % 16 == 0, M * ceil(K/2048) < 2^31; a
+ * launch of 2^32 work-items (a row takes one for each 8 columns, a power of two of them and
+ * 16 at least up to K = 2048, then whole 256s) returns W4A16_ERR_UNSUPPORTED. */
 int w8a8_silu_mul_quant(const void* x, int x_dtype, long long ldx, void* y_out, int y_dtype,
                         void* q, float* scales, int M, int K, w4a16_stream_t stream);
 

@@ -5,6 +5,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 
 import pytest
 
@@ -77,3 +78,20 @@ def test_workspace_query():
                 for D in (64, 128, 256):
                     for n in (0, 1000, 1 << 20, 1 << 30):
                         assert lib.tree_attn_workspace_bytes(B, T, Hq, Hkv, D, n) <= lib.W4A16_WORKSPACE_HEAD_BYTES + (64 << 20)
+
+
+def test_size_limits_are_the_same_for_the_query_and_the_call():
+    assert call(Hq=65538, qs=65538 * 128) == -2 and status(lib.tree_attn_workspace_bytes, 1, 1, 65538, 2, 128, 10) == -2
+    assert call(B=1 << 20, T=1, Hq=32, Hkv=8, qs=4096) == -2
+    assert status(lib.tree_attn_workspace_bytes, 1 << 20, 1, 32, 8, 128, 10) == -2
+    # A launch of 2^32 work-items, whatever the kernel (calls in a process that sees no GPU: -7 is a launch that failed there).
+    code = ("import ctypes, bit_weight_only_03_amd as L\n"
+            "lib, b, p = L._lib_get(), ctypes.c_size_t(), 4096\n"
+            "for B, T, Hq, Hkv, D in ((1 << 24, 1, 1, 1, 64), (1 << 20, 64, 16, 1, 256), (1 << 22, 64, 1, 1, 64), (1 << 24, 1, 1, 1, 256)):\n"
+            "    print(lib.tree_attn_workspace_bytes(B, T, Hq, Hkv, D, 10, ctypes.byref(b)), lib.tree_attn(p, Hq * D, p, p, 1, 1, 16, 0, D, 0,\n"
+            "          p, 1000, p, 10, p, 0.1, p, None, B, T, Hq, Hkv, D, p, 1 << 40, None))\n")
+    out = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, HIP_VISIBLE_DEVICES="-1"), capture_output=True, text=True,
+                         timeout=300, cwd=ROOT)
+    assert out.returncode == 0, out.stderr[-500:]
+    got = [tuple(int(v) for v in line.split()) for line in out.stdout.strip().split("\n")[-4:]]
+    assert got == [(-6, -6), (-6, -6), (0, -7), (0, -7)]

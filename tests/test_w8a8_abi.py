@@ -150,3 +150,9 @@ def test_gemm_long_sums_over_many_columns_have_a_plan():
 def test_gemm_size_query_refuses_what_the_call_refuses():
     for got in gemm_statuses_without_a_device((1, 2**31 - 8, 16), (1 << 26, 1 << 14, 16)):
         assert got == (-6, -6), got
+
+
+def test_row_operators_refuse_launches_past_their_size():
+    assert norm(M=1 << 26, K=16, ldx=16) == -6 and norm(M=1 << 22, K=8192, ldx=8192) == -6
+    assert gated(M=1 << 28, K=16, ldx=32) == -6 and gated(M=1 << 24, K=2048, ldx=4096) == -6
+    assert gated(K=(1 << 30) + 16, ldx=1 << 32) == -2
