@@ -355,3 +355,90 @@ def test_parts_of_an_odd_number_of_rows_and_splits_are_aligned():
     want = (f[:, :, None] * o).sum(1) / (f * l).sum(1, keepdim=True)
     assert torch.all((out.cpu().double()[0] - want).abs() <= UT["bf16"] * want.abs() + 64 * U * (f[:, :, None] * o).abs().sum(1) / (f * l).sum(1, keepdim=True))
     c.check(out, lse)
+
+
+def check_units(c, out, lse):
+    """Case.check over the rows of a request and kv head at once (the same definition and tolerances, for larger cases)."""
+    T, G, D = c.T, c.Hq // c.Hkv, c.D
+    out = out.cpu().double().view(c.B, T, c.Hkv, G, D)
+    lse = lse.cpu().double().view(c.B, T, c.Hkv, G)
+    q = c.q[:, :c.Hq * D].double().view(c.B, T, c.Hkv, G, D)
+    for b in range(c.B):
+        sees = c.sees(b)[:, None, :].expand(T, G, -1).reshape(T * G, -1)
+        some = sees.any(1)
+        k, v = (x.double() for x in c.dense[b])
+        for h in range(c.Hkv):
+            rows = q[b, :, h].reshape(T * G, D)
+            a = (rows @ k[:, h].t() * c.scale).masked_fill(~sees, -math.inf)
+            mag = (rows.abs() @ k[:, h].abs().t() * c.scale).masked_fill(~sees, 0)
+            want_lse = torch.logsumexp(a, 1)
+            p = torch.exp(a - torch.where(some, want_lse, 0.0)[:, None])
+            o = p @ v[:, h]
+            e = (D + 4) * U * mag.amax(1) + 4 * U * (a.abs().masked_fill(~sees, 0).amax(1) + 4) + (sees.sum(1) + 64) * U
+            tol = (UT[c.dtype] + 2 * e)[:, None] * (p @ v[:, h].abs()) + UT[c.dtype] * o.abs() + 2.0 ** -25
+            err = (out[b, :, h].reshape(T * G, D) - o).abs()
+            assert torch.all(err <= tol), (b, h, float((err / tol).max()), (err > tol).nonzero()[:4].tolist())
+            got = lse[b, :, h].reshape(T * G)
+            assert torch.all(out[b, :, h].reshape(T * G, D)[~some] == 0) and torch.all(torch.isneginf(got[~some]))
+            assert torch.all(((got - want_lse).abs() <= e + 2 * U * want_lse.abs())[some])
+
+
+# Every kernel, with the keys whole and split and with several blocks of rows, over enough tiles that each ring slot is
+# filled again several times: 9 tiles a group of waves at least where a ring is four deep, 4 where it is two.
+KERNELS = [
+    # B, T, Hq, Hkv, D, len, page -> rows and key groups of a workgroup, split, blocks of rows
+    (1, 1, 1, 1, 64, 700, 16, 16, 4, False, 1), (64, 1, 1, 1, 64, 4097, 64, 16, 4, True, 1), (1, 21, 1, 1, 64, 500, 32, 16, 4, False, 2),
+    (96, 21, 3, 3, 64, 500, 16, 32, 4, False, 1), (32, 33, 1, 1, 64, 4097, 32, 32, 4, True, 2), (96, 33, 2, 2, 64, 500, 64, 32, 4, False, 2),
+    (96, 33, 3, 3, 64, 700, 16, 64, 2, False, 1), (96, 33, 1, 1, 64, 4097, 32, 64, 2, True, 1), (96, 13, 10, 2, 64, 700, 8, 64, 2, False, 2),
+    (96, 13, 15, 3, 64, 333, 16, 128, 1, False, 1), (48, 33, 9, 3, 64, 2100, 64, 128, 1, True, 1), (96, 21, 16, 2, 64, 333, 4, 128, 1, False, 2),
+    (1, 5, 1, 1, 128, 700, 32, 16, 4, False, 1), (32, 1, 1, 1, 128, 4097, 16, 16, 4, True, 1), (1, 21, 1, 1, 128, 500, 64, 16, 4, False, 2),
+    (48, 21, 3, 3, 128, 500, 8, 32, 4, False, 1), (16, 33, 1, 1, 128, 4097, 64, 32, 4, True, 2), (96, 33, 1, 1, 128, 500, 16, 32, 4, False, 2),
+    (1, 8, 40, 8, 128, 8192, 64, 32, 4, True, 2), (1, 4, 40, 8, 128, 20000, 32, 32, 4, True, 1),
+    (48, 33, 3, 3, 128, 700, 32, 64, 2, False, 1), (24, 33, 1, 1, 128, 6000, 64, 64, 2, True, 1), (96, 13, 5, 1, 128, 700, 16, 64, 2, False, 2),
+    (96, 1, 3, 3, 128, 333, 2, 128, 1, False, 1), (32, 13, 5, 1, 128, 3000, 32, 128, 1, True, 1), (96, 21, 8, 1, 128, 333, 16, 128, 1, False, 2),
+    (1, 1, 1, 1, 256, 333, 16, 16, 2, False, 1), (16, 1, 1, 1, 256, 4097, 32, 16, 2, True, 1), (1, 4, 5, 1, 256, 333, 64, 16, 2, False, 2),
+    (48, 4, 15, 3, 256, 333, 8, 64, 1, False, 1), (24, 4, 5, 1, 256, 3000, 16, 64, 1, True, 1), (24, 21, 8, 1, 256, 333, 32, 64, 1, False, 3),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,n,page,rows,groups,split,row_blocks", KERNELS)
+def test_each_kernel_over_many_tiles(dtype, B, T, Hq, Hkv, D, n, page, rows, groups, split, row_blocks):
+    g = torch.Generator().manual_seed(n + B)
+    # the first request has the whole length; of the others some have little or nothing: fewer tiles than splits
+    lens = [n] + [int(torch.randint(0, n + 1, (1,), generator=g)) if b % 5 else b % 7 for b in range(1, B)]
+    c = Case(B, T, Hq, Hkv, D, page, dtype, lens, seed=n)
+    c.mask[B // 2, ::3] = 0                     # some rows see their context alone
+    out, lse = c.run()
+    ran = dict(f.split("=") for f in L.w4a16_last_variant().split()[1:])
+    assert (int(ran["rows"]), int(ran["groups"]), int(ran["splits"]) > 1, int(ran["row_blocks"])) == (rows, groups, split, row_blocks), ran
+    tiles = -(-(n + T) // 32)
+    assert tiles // int(ran["splits"]) // groups >= (4 if rows <= 32 else 9), ran
+    check_units(c, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,n,page,rows,groups,split,row_blocks", [k for k in KERNELS if k[1] > 2])
+def test_each_kernel_keeps_what_is_not_seen_out(dtype, B, T, Hq, Hkv, D, n, page, rows, groups, split, row_blocks):
+    # Draft 1 is seen by nobody and holds NaN and infinities; then draft 0 has an infinity in one column of v, which
+    # becomes the result's for the rows that see it and changes no bit of any other.
+    c = Case(B, T, Hq, Hkv, D, page, dtype, [n if b % 3 == 0 else (7 * b) % 64 for b in range(B)], seed=n)
+    c.mask &= ~np.uint64(2)
+    want, want_lse = c.run()
+    for b in range(B):
+        k, v = c.dense[b]
+        at = int(c.lens[b])
+        k[at + 1], v[at + 1, :, ::2], v[at + 1, :, 1::2] = float("nan"), float("inf"), float("nan")
+    c.store()
+    out, lse = c.on_gpu().run()
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse.view(torch.int32), want_lse.view(torch.int32))
+    for b in range(B):
+        c.dense[b][1][int(c.lens[b]), :, D - 3] = float("inf")
+    c.store()
+    out, lse = c.on_gpu().run()
+    assert torch.equal(lse.view(torch.int32), want_lse.view(torch.int32))
+    sees = torch.from_numpy((c.mask & np.uint64(1)) != 0).view(B * T, 1).expand(B * T, Hq)
+    out, want = out.cpu(), want.cpu()
+    assert torch.all(out[..., D - 3][sees] == float("inf"))
+    out[..., D - 3][sees] = want[..., D - 3][sees]
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
