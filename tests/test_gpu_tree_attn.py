@@ -417,6 +417,51 @@ def test_each_kernel_over_many_tiles(dtype, B, T, Hq, Hkv, D, n, page, rows, gro
     check_units(c, out, lse)
 
 
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,page,dtype,lens,heads_first,q_pad", CASES)
+def test_a_looser_bound_on_the_lengths(B, T, Hq, Hkv, D, page, dtype, lens, heads_first, q_pad):
+    # Planned for far longer contexts than there are: splits with no tiles, parts that have seen nothing.
+    c = Case(B, T, Hq, Hkv, D, page, dtype, lens, seed=T + Hq + D, heads_first=heads_first, q_pad=q_pad)
+    some_split = False
+    for more in (4096, 60000):
+        table = torch.full((B, -(-(c.max_len + more + T) // page)), 10 ** 9, dtype=torch.int32)   # past a request's pages: anything
+        table[:, :c.table.shape[1]] = c.table[:, :table.shape[1]]
+        wide = Case(B, T, Hq, Hkv, D, page, dtype, lens, seed=T + Hq + D, heads_first=heads_first, q_pad=q_pad)
+        wide.table = table
+        out, lse = wide.run(max_len=c.max_len + more)
+        some_split |= "splits=1 " not in L.w4a16_last_variant()
+        c.check(out, lse)
+    assert some_split
+
+
+def test_graph_replays_match_the_definition():
+    # One capture, planned for 900 tokens, replayed for other lengths with the program's own calls between the replays.
+    c = Case(2, 4, 10, 2, 128, 32, "bf16", [900, 900], seed=3)
+    work = torch.zeros(L.tree_attn_workspace_bytes(2, 4, 10, 2, 128, 900), dtype=torch.uint8, device=DEV)
+    assert work.numel() > L.W4A16_WORKSPACE_HEAD_BYTES
+    c.run(work=work)
+    torch.cuda.synchronize()
+    out = torch.empty(8, 10, 128, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(8, 10, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        c.run(work=work, stream=s, out=out, lse_out=lse)
+    full = c.dense
+    for lens in ([900, 900], [1, 900], [0, 0], [333, 31], [900, 2]):
+        c.lens = torch.tensor(lens, dtype=torch.int32)
+        c.dense = [[d[:n + 4] for d in full[b]] for b, n in enumerate(lens)]   # the drafts are what the cache holds after n
+        c.g["lens"].copy_(c.lens)
+        out.fill_(float("nan"))
+        lse.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_units(c, out, lse)
+        eager = c.run(work=work)
+        torch.cuda.synchronize()
+        assert torch.equal(eager[0].view(torch.int16), out.view(torch.int16))
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("B,T,Hq,Hkv,D,n,page,rows,groups,split,row_blocks", [k for k in KERNELS if k[1] > 2])
 def test_each_kernel_keeps_what_is_not_seen_out(dtype, B, T, Hq, Hkv, D, n, page, rows, groups, split, row_blocks):
