@@ -413,3 +413,18 @@ def test_gated_where_the_reciprocal_is_subnormal():
     y = torch.empty(1, K, device=DEV)
     L.w8a8_silu_mul_quant(x.to(DEV), "f32", 2 * K, y, "f32", None, None, 1, K)
     assert torch.all((y.cpu().double()[0, :n] - want).abs() <= (64 * U + 2.0 ** -21) * want.abs())
+
+
+# From 2^24 elements on the results are stored past the caches: kernels of their own.
+@pytest.mark.parametrize("M,K,xd,rd,wd,yd,pad", [
+    (4099, 4112, "bf16", "bf16", "f32", "bf16", 8), (1823, 9232, "f16", "f32", "f16", "f16", 0), (521, 32768, "f32", "bf16", "bf16", "f32", 16),
+])
+def test_norm_of_large_results(M, K, xd, rd, wd, yd, pad):
+    assert M * K >= 1 << 24
+    test_norm_matches_definition(M, K, xd, rd, wd, yd, pad)
+
+
+@pytest.mark.parametrize("M,K,xd,yd,pad", [(4099, 4112, "bf16", "f16", 8), (116521, 144, "f16", "bf16", 0), (1031, 17408, "f32", "f32", 0)])
+def test_gated_of_large_results(M, K, xd, yd, pad):
+    assert M * K >= 1 << 24
+    test_gated_matches_definition(M, K, xd, yd, pad)
