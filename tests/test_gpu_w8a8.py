@@ -428,3 +428,21 @@ def test_norm_of_large_results(M, K, xd, rd, wd, yd, pad):
 def test_gated_of_large_results(M, K, xd, yd, pad):
     assert M * K >= 1 << 24
     test_gated_matches_definition(M, K, xd, yd, pad)
+
+
+def test_gated_where_the_exponent_is_past_every_range():
+    # -g log2(e) itself overflows from 2.36e38 on: the result is still g or 0, and NaN only for -infinity and NaN.
+    K = 128
+    gate = torch.zeros(1, K)
+    big = [3.3e38, -3.3e38, 2.4e38, -2.4e38, 2.3e38, -2.3e38, 104.0, -104.0, 150.0, -150.0, 87.3, 126.0, float("inf"), float("-inf"), float("nan")]
+    gate[0, :len(big)] = torch.tensor(big)
+    y = torch.empty(1, K, device=DEV)
+    L.w8a8_silu_mul_quant(torch.cat([gate, torch.ones(1, K)], 1).to(DEV), "f32", 2 * K, y, "f32", None, None, 1, K)
+    y = y.cpu()[0]
+    for i, v in enumerate(big):
+        if v != v or v == float("-inf"):
+            assert torch.isnan(y[i]), v
+        elif v > 0:
+            assert y[i] == gate[0, i], (v, float(y[i]))
+        else:
+            assert y[i] == 0, (v, float(y[i]))
