@@ -145,12 +145,14 @@ __device__ __forceinline__ size_t out_row(const TreeArgs& a, uint32_t b, uint32_
 
 // Scores, maxima, sums and O are fp32.  The probabilities are rounded to the
 // type of q, k and v, as the matrix unit takes them (the sum l adds them
-// before that): one rounding of 2^-9 (bf16) or 2^-12 (f16) per key, averaged over
-// the keys.
+// before that): a rounding of at most 2^-8 (bf16) or 2^-11 (f16) of each key's
+// probability, averaged over the keys.  Results are off by 0.0022 of their size in
+// bf16 (f16 0.00021), where rounding them alone gives 0.0017 (0.00019).
 //
 // One token over 150000 keys (614 MB of cache) takes 104 us, 5.9 TB/s: bound by
-// memory, two workgroups of four key groups per CU.  Four requests of 16 drafts
-// over up to 4097 keys (54 MB, 80 rows a kv head) take 26 us and the merge 5:
+// memory, one workgroup of four key groups per CU (its rings take 128 of the CU's
+// 160 KiB of LDS).  Four requests of 16 drafts
+// over up to 4097 keys (54 MB, 80 rows a kv head) take 26 us and the merge 6:
 // there a CU has one workgroup of four waves, each step (1.3 us) is a chain of
 // LDS reads, scores, maxima, exponentials and the product with V that nothing
 // overlaps.  Eight ring stages, eight waves in two key groups, non-temporal
@@ -166,7 +168,10 @@ __global__ __launch_bounds__(WK* WR * 64, 2) void tree_attn_kernel(TreeArgs a) {
     constexpr int kKeys = 512 / D;             // keys per load instruction
     constexpr int kPer = kTile / kKeys / WR;   // loads of K (and of V) per wave and tile
     constexpr int kRows = 16 * RT * WR;
-    constexpr int kAux = WR < 4 ? kAuxNT : 0;  // few rows: read once; more: other blocks of rows read it again
+    // Non-temporal loads where few rows share the keys: 106 us against 117 for one token over 150000 keys, 33.5 against 36
+    // for 4 drafts over 32768.  (With two blocks of rows, which read the same keys, 8 drafts over 8192 take 18.9 against 18.1.)
+    // Where four waves share them, 31.7 us against 31.3 for 4 x 16 drafts over 4097: ordinary ones.
+    constexpr int kAux = WR < 4 ? kAuxNT : 0;
     static_assert(kPer >= 1, "a wave loads whole instructions");
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;

@@ -41,10 +41,11 @@ __device__ __forceinline__ float wave_sum(float v) {
 // workgroup, its waves' sums joined through LDS (a wave per row and four rows
 // per workgroup took as long for K = 256 .. 1024).  NT: results bypass the
 // caches' retention where they are larger than what the next kernel could find
-// there (2560 x 16384: 58 against 64 us; 8192 x 5120: 70 against 72).
-// Bound by memory: 8192 x 5120 with residual moves 294 MB in 67 us, 4.4 TB/s,
+// there (2560 x 16384: 55 against 62 us; 8192 x 5120: 65 against 67; 2048 x 5120,
+// below the limit, 16.1 against 16.5, but there the next kernel finds them).
+// Bound by memory: 8192 x 5120 with residual moves 295 MB in 65 us, 4.5 TB/s,
 // where a 1 GiB copy reaches 4.8.  More vectors per lane and fewer waves were
-// slower (P = 2: 70, 4: 84, 10: 103 us): they only delay the first store.
+// slower (when P = 1 took 67 us, P = 2 took 70, 4: 84, 10: 103): they only delay the first store.
 template <int P, bool NT>
 __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormArgs a) {
     const int t = threadIdx.x, threads = blockDim.x;
@@ -143,7 +144,8 @@ constexpr int kGatedCols = kGatedThreads * 8;
 
 // A workgroup takes 2048 columns of one row, or several short rows (a power of
 // two of lanes each, 16 at least); a block of 128 columns is 16 lanes.  Bound by
-// memory: 4096 x 17408 moves 359 MB in 65 us, 5.5 TB/s.
+// memory: 4096 x 17408 moves 359 MB in 68 us, 5.3 TB/s, with results stored past
+// the caches or not.
 template <bool NT>
 __global__ __launch_bounds__(kGatedThreads) void silu_mul_quant_kernel(GatedArgs a) {
     const unsigned chunk = blockIdx.x % (unsigned)a.chunks;
