@@ -115,7 +115,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(NormArgs a) {
 // rest of the constant, so that 2^t keeps its relative error for large |g|.
 // exp(-g) past fp32's range is infinite and the result 0, as in the formula.
 // The reciprocal unit flushes a result below 2^-126 to zero, so it takes
-// (1 + p) / 16: 1 / (1 + p) is subnormal from g = -87.3 on, its product with g is not.
+// (1 + p) / 16: 1 / (1 + p) is subnormal from g = -87.3 on, its product with g is not
+// (4096 x 17408: 68.3 us against 67.4 without; a branch for such waves took as long).
 __device__ __forceinline__ float silu(float g) {
     constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
     const float t = -g * kLog2e;
