@@ -1,6 +1,7 @@
 """Thin Python binding of libw4a16.so, the gfx950 W4A16 / ternary small-M
 linear-layer library (C ABI declared in include/w4a16.h, the 8-bit layer's in
-include/w8a8.h, the draft-tree attention's in include/tree_attn.h).
+include/w8a8.h, the draft-tree attention's in include/tree_attn.h, rotary
+positions and the append to the cache in include/rope_append.h).
 
 Every function here has the same name and argument order as its C entry
 point and only marshals arguments: tensors (anything with ``data_ptr()``) or
@@ -64,7 +65,7 @@ _SIGS = {
     "w4a16_plan_variant": [_I, _I, _I, _I, _I, ctypes.c_char_p, _SZ],
     "w4a16_last_error": [],
 }
-# include/w8a8.h and include/tree_attn.h
+# include/w8a8.h, include/tree_attn.h, include/rope_append.h
 _L = ctypes.c_longlong
 _F = ctypes.c_float
 _SIGS_W8A8 = {
@@ -77,6 +78,12 @@ _SIGS_TREE = {
     "tree_attn_workspace_bytes": [_I, _I, _I, _I, _I, _I, _PSZ],
     "tree_attn": [_P, _L, _P, _P, _I, _I, _I, _L, _L, _L, _P, _I, _P, _I, _P, _F, _P, _P, _I, _I, _I,
                   _I, _I, _P, _SZ, _P],
+}
+_D = ctypes.c_double
+_SIGS_ROPE = {
+    "rope_frequencies": [ctypes.POINTER(_F), _I, _D, _D, _D, _D, _D],
+    "rope_append": [_P, _L, _P, _L, _P, _L, _I, _P, _P, _I, _I, _F, _P, _L, _P, _P, _I, _I, _L, _L, _L, _P, _I, _I, _I,
+                    _I, _P],
 }
 _STR_RESULT = ("w4a16_status_string", "w4a16_last_variant", "w4a16_last_error")
 
@@ -92,7 +99,7 @@ def _lib_get():
             raise ImportError(f"{LIB_PATH} is missing: build it with "
                               "`python -m bit_weight_only_03_amd.build`")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, args in (*_SIGS.items(), *_SIGS_W8A8.items(), *_SIGS_TREE.items()):
+        for name, args in (*_SIGS.items(), *_SIGS_W8A8.items(), *_SIGS_TREE.items(), *_SIGS_ROPE.items()):
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = ctypes.c_char_p if name in _STR_RESULT else _I
@@ -112,6 +119,7 @@ _lib = _LazyLib()
 EXPORTED = tuple(_SIGS)
 EXPORTED_W8A8 = tuple(_SIGS_W8A8)
 EXPORTED_TREE = tuple(_SIGS_TREE)
+EXPORTED_ROPE = tuple(_SIGS_ROPE)
 
 
 def _ptr(t):
@@ -379,3 +387,20 @@ def tree_attn(q, q_stride, k, v, dtype, num_pages, page_size, page_stride, token
         workspace_bytes, _stream(stream))
     if rc:
         _check("tree_attn", rc)
+
+
+def rope_frequencies(rot_dim: int, base: float, factor=1.0, original=0.0, slow=1.0, fast=32.0) -> list:
+    f = (_F * max(rot_dim // 2, 1))()
+    _check("rope_frequencies", _lib.rope_frequencies(f, rot_dim, base, factor, original, slow, fast))
+    return list(f)
+
+
+def rope_append(q, q_stride, k, k_stride, v, v_stride, dtype, positions, inv_freq, rot_dim, interleaved, gain, q_out,
+                q_out_stride, k_cache, v_cache, num_pages, page_size, page_stride, token_stride, head_stride, slots, M,
+                Hq, Hkv, D, stream=None):
+    rc = _lib.rope_append(
+        _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _dt_of[dtype], _ptr(positions), _ptr(inv_freq), rot_dim,
+        interleaved, gain, _ptr(q_out), q_out_stride, _ptr(k_cache), _ptr(v_cache), num_pages, page_size, page_stride,
+        token_stride, head_stride, _ptr(slots), M, Hq, Hkv, D, _stream(stream))
+    if rc:
+        _check("rope_append", rc)
