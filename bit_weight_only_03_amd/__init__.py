@@ -1,7 +1,8 @@
 """Thin Python binding of libw4a16.so, the gfx950 W4A16 / ternary small-M
 linear-layer library (C ABI declared in include/w4a16.h, the 8-bit layer's in
 include/w8a8.h, the draft-tree attention's in include/tree_attn.h, rotary
-positions and the append to the cache in include/rope_append.h).
+positions and the append to the cache in include/rope_append.h, the low-rank
+adapters' in include/lora.h).
 
 Every function here has the same name and argument order as its C entry
 point and only marshals arguments: tensors (anything with ``data_ptr()``) or
@@ -65,7 +66,7 @@ _SIGS = {
     "w4a16_plan_variant": [_I, _I, _I, _I, _I, ctypes.c_char_p, _SZ],
     "w4a16_last_error": [],
 }
-# include/w8a8.h, include/tree_attn.h, include/rope_append.h
+# include/w8a8.h, include/tree_attn.h, include/rope_append.h, include/lora.h
 _L = ctypes.c_longlong
 _F = ctypes.c_float
 _SIGS_W8A8 = {
@@ -85,6 +86,10 @@ _SIGS_ROPE = {
     "rope_append": [_P, _L, _P, _L, _P, _L, _I, _P, _P, _I, _I, _F, _P, _L, _P, _P, _I, _I, _L, _L, _L, _P, _I, _I, _I,
                     _I, _P],
 }
+_SIGS_LORA = {
+    "lora_workspace_bytes": [_I, _I, _I, _I, _I, _PSZ],
+    "lora_add": [_P, _I, _L, _P, _P, _P, _P, _I, _P, _P, _P, _I, _L, ctypes.POINTER(_I), _I, _I, _I, _I, _I, _P, _SZ, _P],
+}
 _STR_RESULT = ("w4a16_status_string", "w4a16_last_variant", "w4a16_last_error")
 
 _lib_handle = None
@@ -99,7 +104,8 @@ def _lib_get():
             raise ImportError(f"{LIB_PATH} is missing: build it with "
                               "`python -m bit_weight_only_03_amd.build`")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, args in (*_SIGS.items(), *_SIGS_W8A8.items(), *_SIGS_TREE.items(), *_SIGS_ROPE.items()):
+        for name, args in (*_SIGS.items(), *_SIGS_W8A8.items(), *_SIGS_TREE.items(), *_SIGS_ROPE.items(),
+                           *_SIGS_LORA.items()):
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = ctypes.c_char_p if name in _STR_RESULT else _I
@@ -120,6 +126,7 @@ EXPORTED = tuple(_SIGS)
 EXPORTED_W8A8 = tuple(_SIGS_W8A8)
 EXPORTED_TREE = tuple(_SIGS_TREE)
 EXPORTED_ROPE = tuple(_SIGS_ROPE)
+EXPORTED_LORA = tuple(_SIGS_LORA)
 
 
 def _ptr(t):
@@ -404,3 +411,21 @@ def rope_append(q, q_stride, k, k_stride, v, v_stride, dtype, positions, inv_fre
         token_stride, head_stride, _ptr(slots), M, Hq, Hkv, D, _stream(stream))
     if rc:
         _check("rope_append", rc)
+
+
+def lora_workspace_bytes(M: int, N: int, K: int, R: int, parts: int = 1) -> int:
+    b = _SZ()
+    _check("lora_workspace_bytes", _lib.lora_workspace_bytes(M, N, K, R, parts, ctypes.byref(b)))
+    return b.value
+
+
+def lora_add(x, dtype, ldx, a, b, ranks, scales, n_adapters, adapter, base, y, y_dtype, ldy, part_cols, M, N, K, R,
+             workspace=None, workspace_bytes=0, stream=None):
+    """part_cols: a sequence of the parts' widths, which also gives their number, or None (one part)."""
+    parts = len(part_cols) if part_cols else 1
+    rc = _lib.lora_add(
+        _ptr(x), _dt_of[dtype], ldx, _ptr(a), _ptr(b), _ptr(ranks), _ptr(scales), n_adapters, _ptr(adapter), _ptr(base),
+        _ptr(y), _dt_of[y_dtype], ldy, (_I * parts)(*part_cols) if part_cols else None, parts, M, N, K, R,
+        _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc:
+        _check("lora_add", rc)
