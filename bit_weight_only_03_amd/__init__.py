@@ -2,7 +2,8 @@
 linear-layer library (C ABI declared in include/w4a16.h, the 8-bit layer's in
 include/w8a8.h, the draft-tree attention's in include/tree_attn.h, rotary
 positions and the append to the cache in include/rope_append.h, the low-rank
-adapters' in include/lora.h).
+adapters' in include/lora.h, attention behind a shared prefix in
+include/prefix_attn.h).
 
 Every function here has the same name and argument order as its C entry
 point and only marshals arguments: tensors (anything with ``data_ptr()``) or
@@ -66,7 +67,7 @@ _SIGS = {
     "w4a16_plan_variant": [_I, _I, _I, _I, _I, ctypes.c_char_p, _SZ],
     "w4a16_last_error": [],
 }
-# include/w8a8.h, include/tree_attn.h, include/rope_append.h, include/lora.h
+# include/w8a8.h, include/tree_attn.h, include/rope_append.h, include/lora.h, include/prefix_attn.h
 _L = ctypes.c_longlong
 _F = ctypes.c_float
 _SIGS_W8A8 = {
@@ -90,6 +91,11 @@ _SIGS_LORA = {
     "lora_workspace_bytes": [_I, _I, _I, _I, _I, _PSZ],
     "lora_add": [_P, _I, _L, _P, _P, _P, _P, _I, _P, _P, _P, _I, _L, ctypes.POINTER(_I), _I, _I, _I, _I, _I, _P, _SZ, _P],
 }
+_SIGS_PREFIX = {
+    "prefix_attn_workspace_bytes": [_I, _I, _I, _I, _I, _I, _I, _PSZ],
+    "prefix_attn": [_P, _L, _P, _P, _I, _I, _I, _L, _L, _L, _P, _P, _I, _P, _I, _P, _I, _P, _F, _P, _P, _I, _I, _I, _I, _I,
+                    _P, _SZ, _P],
+}
 _STR_RESULT = ("w4a16_status_string", "w4a16_last_variant", "w4a16_last_error")
 
 _lib_handle = None
@@ -105,7 +111,7 @@ def _lib_get():
                               "`python -m bit_weight_only_03_amd.build`")
         lib = ctypes.CDLL(LIB_PATH)
         for name, args in (*_SIGS.items(), *_SIGS_W8A8.items(), *_SIGS_TREE.items(), *_SIGS_ROPE.items(),
-                           *_SIGS_LORA.items()):
+                           *_SIGS_LORA.items(), *_SIGS_PREFIX.items()):
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = ctypes.c_char_p if name in _STR_RESULT else _I
@@ -127,6 +133,7 @@ EXPORTED_W8A8 = tuple(_SIGS_W8A8)
 EXPORTED_TREE = tuple(_SIGS_TREE)
 EXPORTED_ROPE = tuple(_SIGS_ROPE)
 EXPORTED_LORA = tuple(_SIGS_LORA)
+EXPORTED_PREFIX = tuple(_SIGS_PREFIX)
 
 
 def _ptr(t):
@@ -429,3 +436,21 @@ def lora_add(x, dtype, ldx, a, b, ranks, scales, n_adapters, adapter, base, y, y
         _ptr(workspace), workspace_bytes, _stream(stream))
     if rc:
         _check("lora_add", rc)
+
+
+def prefix_attn_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, D: int, max_prefix: int, max_len: int) -> int:
+    b = _SZ()
+    _check("prefix_attn_workspace_bytes",
+           _lib.prefix_attn_workspace_bytes(B, T, Hq, Hkv, D, max_prefix, max_len, ctypes.byref(b)))
+    return b.value
+
+
+def prefix_attn(q, q_stride, k, v, dtype, num_pages, page_size, page_stride, token_stride, head_stride, prefix_table,
+                prefix_len, max_prefix, block_table, table_stride, lens, max_len, tree_mask, scale, out, lse, B, T, Hq,
+                Hkv, D, workspace=None, workspace_bytes=0, stream=None):
+    rc = _lib.prefix_attn(
+        _ptr(q), q_stride, _ptr(k), _ptr(v), _dt_of[dtype], num_pages, page_size, page_stride, token_stride, head_stride,
+        _ptr(prefix_table), _ptr(prefix_len), max_prefix, _ptr(block_table), table_stride, _ptr(lens), max_len,
+        _ptr(tree_mask), scale, _ptr(out), _ptr(lse), B, T, Hq, Hkv, D, _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc:
+        _check("prefix_attn", rc)

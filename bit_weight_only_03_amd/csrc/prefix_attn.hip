@@ -1,0 +1,822 @@
+// prefix_attn.hip -- attention of a batch that shares a long prefix, over a
+// paged cache.
+//
+// One launch takes two kinds of work side by side, and a second one joins their
+// parts.  Prefix work is bound by the matrix units: the rows of all requests
+// (B T G of a kv head) against the same keys, in blocks of 128 rows whose four
+// waves share tiles of 32 keys in LDS.  Own work is bound by memory: the T G
+// rows of one request against its own keys, whose waves take tiles in turn and
+// load them straight into registers.  Where the prefix is short the own work
+// takes it too (each request reads it again, from the caches), which saves the parts.
+//
+// Products.  Scores are computed transposed, S^T = K Q^T, so that a lane holds one
+// row's scores, in the layout in which O^T = V^T P^T takes P as its B operand
+// once the slots of k are named after the keys that the lane holds.  V^T's
+// columns are free: lane r of operand tile t takes column (D/N) r + t, so it
+// reads consecutive columns of each key and pairs keys up with byte permutes.
+#include "attn_common.h"
+#include "../../include/prefix_attn.h"
+
+using namespace w4k;
+
+namespace {
+
+constexpr int kTile = 32;              // keys per tile
+constexpr int kWaves = 4;
+constexpr int kBlockRows = 32 * kWaves;   // rows of a workgroup of prefix work
+constexpr int kMaxParts = 64;
+constexpr size_t kMaxPartBytes = (size_t)128 << 20;
+
+struct PrefixArgs {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    const int* prefix_table;
+    const int* prefix_len;
+    const int* table;
+    const int* lens;
+    const uint64_t* mask;
+    uint16_t* out;
+    float* lse;
+    float* part_o;     // [row of out][part][D] sums that are not divided yet
+    float2* part_ml;   // [row of out][part] maximum (log2 units) and sum
+    long long q_stride, page_stride, token_stride, head_stride;
+    int num_pages, page_shift, table_stride;
+    int max_prefix, max_len;
+    float scale2;      // |scale| log2(e)
+    uint32_t q_sign;   // the sign bits of two elements of q where scale is negative
+    int B, T, Hq, Hkv, G;
+    int SP, RB;        // prefix work: splits of the keys, blocks of rows; SP = 0: the own work takes the prefix
+    int SO, RO;        // own work: splits, blocks of rows
+    int parts;         // SP + SO
+    uint32_t prefix_groups, own_groups;   // groups of eight workgroups
+};
+
+// Probabilities are 2^(x - m + kLift): in f16 that keeps them normal down to
+// 2^-26 of the largest, where a long context's many small ones would otherwise fall
+// on the subnormal grid.  A row's maximum m is raised only once a score passes it by
+// kSlack, so that O is seldom rescaled: probabilities stay below 2^(kLift + kSlack), in
+// f16's range.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 12.f;
+template <bool BF16>
+constexpr float kSlack = BF16 ? 8.f : 3.f;
+
+typedef float float16_t __attribute__((ext_vector_type(16)));
+
+template <bool BF16>
+__device__ __forceinline__ float16_t mfma32(const u32x4_t& a, const u32x4_t& b, const float16_t& c) {
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(bitcast<bf16x8_t>(a), bitcast<bf16x8_t>(b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(bitcast<half8_t>(a), bitcast<half8_t>(b), c, 0, 0, 0);
+}
+
+// The other half-wave's x beside this one's.
+__device__ __forceinline__ float max2(float x) {
+    auto a = __builtin_amdgcn_permlane32_swap(bitcast<uint32_t>(x), bitcast<uint32_t>(x), false, false);
+    return __builtin_fmaxf(bitcast<float>((uint32_t)a[0]), bitcast<float>((uint32_t)a[1]));
+}
+__device__ __forceinline__ float sum2(float x) {
+    auto a = __builtin_amdgcn_permlane32_swap(bitcast<uint32_t>(x), bitcast<uint32_t>(x), false, false);
+    return bitcast<float>((uint32_t)a[0]) + bitcast<float>((uint32_t)a[1]);
+}
+
+typedef const __attribute__((address_space(4))) int* const_ptr_t;
+
+// The page of position p of a table whose last position is end - 1, by a scalar
+// load (the tables do not change while the kernel runs).
+__device__ __forceinline__ int page_of(const PrefixArgs& a, const int* table, int p, int end) {
+    return min(max(((const_ptr_t)table)[min(p, end - 1) >> a.page_shift], 0), a.num_pages - 1);
+}
+
+// The first of n tiles that part i of s takes (the first n % s parts take one more).
+__device__ __forceinline__ int share(int n, int s, int i) {
+    const int each = (uint32_t)n / (uint32_t)s;
+    return i * each + min(i, n - s * each);
+}
+
+// ------------------------------------------------------------- prefix work
+
+// Workgroup (unit, rb): keys [tile t0, tile t1) of the prefix for kv head unit / SP, rows rb * 128 .. of the B T G.
+template <bool BF16, int D>
+__device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, uint32_t rb, uint8_t* smem) {
+    constexpr int NS = D == 256 ? 2 : 4;       // ring stages
+    constexpr int NT = D / 32;                 // operand tiles of O^T
+    constexpr int KS = D / 16;                 // products per score tile
+    constexpr int kChunks = D / 8;             // 16-byte chunks of a key
+    constexpr int kSwz = kChunks < 16 ? kChunks - 1 : 15;
+    constexpr int kHalf = kTile * D * 2;       // bytes of a tile of K or of V
+    constexpr int kStage = 2 * kHalf;
+    constexpr int kKeys = 512 / D;             // keys per load instruction
+    constexpr int kSpan = kTile / kWaves;      // keys that a wave loads of a tile: in one page
+    constexpr int kPer = kSpan / kKeys;        // its loads of K (and of V)
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, c = lane & 31, hi = lane >> 5;
+    const uint32_t split = unit % (uint32_t)a.SP, kvh = unit / (uint32_t)a.SP;
+    const int P = min(max(a.prefix_len[0], 0), a.max_prefix), tiles = (P + kTile - 1) / kTile;
+    const int t0 = share(tiles, a.SP, split), t1 = share(tiles, a.SP, split + 1);
+    const long long head = kvh * a.head_stride;
+    const uint32_t key_bytes = (uint32_t)(a.token_stride * 2);
+    const int page_mask = (1 << a.page_shift) - 1;
+    const uint32_t page_bytes = (uint32_t)page_mask * key_bytes + D * 2;
+    const int key_in = lane / kChunks, pos = lane % kChunks;
+
+    const uint32_t rows = (uint32_t)a.B * a.T * a.G, row0 = rb * kBlockRows + wave * 32, G = a.G;
+    const uint32_t row = min(row0 + c, rows - 1);      // past the rows: the last one again, not stored
+    const size_t tok = row / G, out_row = tok * a.Hq + kvh * G + row % G;
+    u32x4_t qf[KS];
+    {
+        const uint16_t* const qp = a.q + tok * a.q_stride + (size_t)(kvh * G + row % G) * D;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[s] = *(const u32x4_t*)(qp + 16 * s + 8 * hi);
+    }
+    auto look_up = [&](int n) { return page_of(a, a.prefix_table, min(n, t1 - 1) * kTile + wave * kSpan, P); };
+    // Tile n (past the last one, the last one again: nothing reads it) into its ring slot.
+    auto issue = [&](int n, int page) {
+        uint8_t* const to = smem + (n - t0) % NS * kStage + wave * kPer * 1024;
+        const int first = min(n, t1 - 1) * kTile + wave * kSpan;
+        const uint32_t in_page = (uint32_t)(first & page_mask) * key_bytes;
+        const long long at = (long long)page * a.page_stride + head;
+        const __amdgpu_buffer_rsrc_t rk = make_rsrc(a.k + at, page_bytes), rv = make_rsrc(a.v + at, page_bytes);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const uint32_t key = key_in + i * kKeys, k_off = 16u * (pos ^ ((wave * kSpan + key) & kSwz));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr_t)(to + i * 1024), 16, key * key_bytes + k_off, in_page, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr_t)(to + kHalf + i * 1024), 16, key * key_bytes + 16u * pos, in_page, 0, 0);
+        }
+    };
+    float16_t o[NT];
+    float m = -__builtin_inff(), l = 0.f;
+#pragma unroll
+    for (int d = 0; d < NT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+    int next = 0;
+    if (t0 < t1) {
+        int page[NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) page[n] = look_up(t0 + n);
+#pragma unroll
+        for (int n = 0; n < NS - 1; ++n) issue(t0 + n, page[n]);
+        next = page[NS - 1];
+        wait_loads<(NS - 1) * 2 * kPer>();   // the rows have arrived
+    } else {
+        wait_loads<0>();
+    }
+#pragma unroll
+    for (int s = 0; s < KS; ++s) qf[s] ^= a.q_sign;
+
+    // One tile: scores, probabilities, product with V.  Score i of lane (c, hi) is
+    // that of key 8 (i / 4) + 4 hi + i % 4.  EDGE: some of its keys are past the end.
+    auto tile = [&](auto edge, const uint8_t* kt, const uint8_t* vt, int first) {
+        constexpr bool EDGE = decltype(edge)::value;
+        float16_t x;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const u32x4_t kf = *(const u32x4_t*)(kt + c * D * 2 + 16 * ((2 * s + hi) ^ (c & kSwz)));
+            x = mfma32<BF16>(kf, qf[s], x);
+        }
+        if constexpr (EDGE) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = first + 8 * (i >> 2) + 4 * hi + (i & 3) < P ? x[i] : -__builtin_inff();
+        }
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = __builtin_fmaxf(top, x[i]);
+        const float mn = max2(top) * a.scale2;
+        if (__builtin_amdgcn_ballot_w64(mn > m + kSlack<BF16>)) {
+            const float up = __builtin_fmaxf(m, mn), f = weight_of(m, up);
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < NT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] *= f;
+            m = up;
+        }
+        const float base = m == -__builtin_inff() ? 0.f : m - kLift<BF16>;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.scale2, -base));
+            sum += x[i];
+        }
+        l += sum;   // this lane's keys; the two lanes of a row are added at the end
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u32x4_t pf;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pf[j] = pack2<BF16>(x[8 * h + 2 * j], x[8 * h + 2 * j + 1]);
+            constexpr int VW = NT / 2;   // dwords of a key per lane
+            uint32_t vr[8][VW];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int key = 16 * h + 8 * (j >> 2) + 4 * hi + (j & 3);
+                const uint8_t* const p = vt + key * D * 2 + c * VW * 4;
+                if constexpr (VW == 1) {
+                    vr[j][0] = *(const uint32_t*)p;
+                } else if constexpr (VW == 2) {
+                    const u32x2_t v = *(const u32x2_t*)p;
+                    vr[j][0] = v[0], vr[j][1] = v[1];
+                } else {
+                    const u32x4_t v = *(const u32x4_t*)p;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) vr[j][e] = v[e];
+                }
+                if constexpr (EDGE) {   // 0 times what lies past the end could be NaN
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) vr[j][w] = first + key < P ? vr[j][w] : 0u;
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < NT; ++d) {
+                u32x4_t va;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    va[j] = __builtin_amdgcn_perm(vr[2 * j + 1][d >> 1], vr[2 * j][d >> 1], d & 1 ? 0x07060302u : 0x05040100u);
+                o[d] = mfma32<BF16>(va, pf, o[d]);
+            }
+        }
+    };
+    auto step = [&](auto edge, int n) {
+        wait_loads<(NS - 2) * 2 * kPer>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        issue(n + NS - 1, next);
+        next = look_up(n + NS);
+        if (row0 >= rows) return;   // a wave without rows only loads
+        const uint8_t* const kt = smem + (n - t0) % NS * kStage;
+        tile(edge, kt, kt + kHalf, n * kTile);
+    };
+    int n = t0;
+    for (const int plain = min(t1, P / kTile); n < plain; ++n) step(std::false_type{}, n);
+    for (; n < t1; ++n) step(std::true_type{}, n);
+    wait_loads<0>();   // nothing may land in LDS after the workgroup's end
+    if (row0 + c >= rows) return;
+    l = sum2(l);
+    const size_t part = out_row * a.parts + split;
+    if (hi == 0) a.part_ml[part] = float2{m, l};
+    // o[d][i] is column NT (8 (i / 4) + 4 hi + i % 4) + d.
+    float* const to = a.part_o + part * D;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float* const p = to + NT * (8 * (i >> 2) + 4 * hi + (i & 3));
+        if constexpr (NT == 2) {
+            *(float2*)p = float2{o[0][i], o[1][i]};
+        } else {
+#pragma unroll
+            for (int d = 0; d < NT; d += 4) *(float4_t*)(p + d) = float4_t{o[d][i], o[d + 1][i], o[d + 2][i], o[d + 3][i]};
+        }
+    }
+}
+
+// ---------------------------------------------------------------- own work
+
+// Workgroup (id, rb): request, kv head and split id; rows rb * 16 RT .. of the request's T G.  Tiles are the
+// prefix's (where SP = 0) and the request's own; wave w takes tiles t0 + w, t0 + w + 4, ..
+template <bool BF16, int D, int RT>
+__device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint32_t rb, uint8_t* smem) {
+    constexpr int DT = D / 16, KS = D / 32;
+    constexpr int VW = D / 32;            // dwords of a key of V per lane
+    constexpr int kRows = 16 * RT;
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63, c = lane & 15, g = lane >> 4;
+    const uint32_t split = id % (uint32_t)a.SO, unit = id / (uint32_t)a.SO, kvh = unit % (uint32_t)a.Hkv, b = unit / (uint32_t)a.Hkv;
+    const int len = min(max(a.lens[b], 0), a.max_len), own_tiles = (len + a.T + kTile - 1) / kTile;
+    const int P = a.SP ? 0 : min(max(a.prefix_len[0], 0), a.max_prefix), prefix_tiles = (P + kTile - 1) / kTile;
+    const int tiles = prefix_tiles + own_tiles;
+    const int t0 = share(tiles, a.SO, split), t1 = share(tiles, a.SO, split + 1);
+    const int* const own_table = a.table + (size_t)b * a.table_stride;
+    const long long head = kvh * a.head_stride;
+    const uint32_t key_bytes = (uint32_t)(a.token_stride * 2);
+    const int page_mask = (1 << a.page_shift) - 1;
+    const uint32_t page_bytes = (uint32_t)page_mask * key_bytes + D * 2;
+
+    // The rows: B operand of the scores, and each row's mask.
+    const uint32_t R = (uint32_t)a.T * a.G, G = a.G, row0 = rb * kRows;
+    u32x4_t qf[RT][KS];
+    uint64_t see[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const uint32_t row = min(row0 + 16 * rt + c, R - 1);   // past the rows: the last one again, not stored
+        const size_t tok = (size_t)b * a.T + row / G;
+        see[rt] = a.mask[tok] & (~0ull >> (64 - a.T));
+        const uint16_t* const qp = a.q + tok * a.q_stride + (size_t)(kvh * G + row % G) * D;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[rt][s] = *(const u32x4_t*)(qp + 32 * s + 8 * g) ^ a.q_sign;
+    }
+    float4_t o[RT][DT];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = -__builtin_inff(), l[rt] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[rt][d] = float4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    bool any_odd = false;   // the same for the whole wave
+
+    // A tile's place: halves of 16 keys lie in one page each (pages have 16 or more).
+    struct Place {
+        int first, len, T;      // its first position, context and drafts of its segment
+        long long at[2];        // elements from the cache's start to the halves' pages
+        uint32_t in_page[2];    // bytes
+    };
+    // In order: the tiles of nothing but prefix, of nothing but context, the prefix's
+    // last one where it ends inside, and the request's with its end and the drafts.
+    const int prefix_whole = P / kTile, whole = prefix_whole + len / kTile, prefix_rest = prefix_tiles - prefix_whole;
+    auto place = [&](int i) {
+        Place p;
+        const bool shared = i < prefix_whole || (prefix_rest && i == whole);
+        const int own = i - (i < whole ? prefix_whole : prefix_tiles);
+        p.first = (shared ? min(i, prefix_whole) : own) * kTile;
+        p.len = shared ? P : len, p.T = shared ? 0 : a.T;
+        const int* const table = shared ? a.prefix_table : own_table;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = p.first + 16 * h;
+            p.at[h] = (long long)page_of(a, table, at, p.len + p.T) * a.page_stride + head;
+            p.in_page[h] = (uint32_t)(at & page_mask) * key_bytes;
+        }
+        return p;
+    };
+    u32x4_t kf[2][KS];
+    uint32_t vr[8][VW];
+    auto load_k = [&](const Place& p) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const __amdgpu_buffer_rsrc_t r = make_rsrc(a.k + p.at[h], page_bytes);
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                kf[h][s] = bitcast<u32x4_t>(__builtin_amdgcn_raw_buffer_load_b128(r, c * key_bytes + 16 * g + 64 * s, p.in_page[h], 0));
+        }
+    };
+    auto load_v = [&](const Place& p) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int h = i >> 2;
+            const __amdgpu_buffer_rsrc_t r = make_rsrc(a.v + p.at[h], page_bytes);
+            const uint32_t off = (4 * g + (i & 3)) * key_bytes + c * VW * 4;
+            if constexpr (VW == 2) {
+                const u32x2_t v = bitcast<u32x2_t>(__builtin_amdgcn_raw_buffer_load_b64(r, off, p.in_page[h], 0));
+                vr[i][0] = v[0], vr[i][1] = v[1];
+            } else {
+#pragma unroll
+                for (int w = 0; w < VW; w += 4) {
+                    const u32x4_t v = bitcast<u32x4_t>(__builtin_amdgcn_raw_buffer_load_b128(r, off + 4 * w, p.in_page[h], 0));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) vr[i][w + e] = v[e];
+                }
+            }
+        }
+    };
+    // One tile; its keys are in registers, its values and the next tile's keys on their way.
+    // EDGE: some of its keys are drafts or past the end.
+    auto tile = [&](auto edge, const Place& p, const Place& next, bool more) {
+        constexpr bool EDGE = decltype(edge)::value;
+        float4_t sc[2][RT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                sc[h][rt] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) sc[h][rt] = mfma<BF16>(kf[h][s], qf[rt][s], sc[h][rt]);
+            }
+        if (more) load_k(next);
+        u32x4_t pf[RT];
+        const int d0 = p.first - p.len;   // the tile's first key among the drafts (negative: context)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][rt][i & 3];
+            if constexpr (EDGE) {
+                const uint32_t bits = visible(p.T ? see[rt] : 0, d0) >> (4 * g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] = (bits >> (16 * (i >> 2) + (i & 3))) & 1u ? x[i] : -__builtin_inff();
+            }
+            float top = x[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, x[i]);
+            const float mn = max4(top) * a.scale2;
+            if (__builtin_amdgcn_ballot_w64(mn > m[rt] + kSlack<BF16>)) {
+                const float up = __builtin_fmaxf(m[rt], mn), f = weight_of(m[rt], up);
+                l[rt] *= f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) o[rt][d][q] *= f;
+                m[rt] = up;
+            }
+            const float base = m[rt] == -__builtin_inff() ? 0.f : m[rt] - kLift<BF16>;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.scale2, -base));
+                sum += x[i];
+            }
+            l[rt] += sum;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pf[rt][j] = pack2<BF16>(x[2 * j], x[2 * j + 1]);
+        }
+        if constexpr (EDGE) {
+            // Keys past the end count as zeros.  A draft's infinity or NaN must not
+            // reach the rows that do not see it (0 * inf): it is taken out of the
+            // product, and given to the rows that do after the loop.
+            uint32_t odd = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool there = d0 + 16 * (i >> 2) + 4 * g + (i & 3) < p.T;
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    vr[i][w] = there ? vr[i][w] : 0u;
+                    odd |= overflow<BF16>(vr[i][w]);
+                }
+            }
+            if (__builtin_amdgcn_ballot_w64((odd & 0x80008000u) != 0)) {
+                any_odd = true;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool draft = d0 + 16 * (i >> 2) + 4 * g + (i & 3) >= 0;   // context goes in as it is
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) {
+                        const uint32_t bad = overflow<BF16>(vr[i][w]) & 0x80008000u;
+                        vr[i][w] &= draft ? ~((bad >> 15) * 0xffffu) : ~0u;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            u32x4_t va;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                va[j] = __builtin_amdgcn_perm(vr[2 * j + 1][d >> 1], vr[2 * j][d >> 1], d & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) o[rt][d] = mfma<BF16>(va, pf[rt], o[rt][d]);
+        }
+        if (more) load_v(next);
+    };
+    int i = t0 + wave;
+    if (i < t1) {
+        Place p = place(i);
+        load_k(p);
+        load_v(p);
+#pragma unroll 1
+        for (; i < min(t1, whole); i += kWaves) {
+            const bool more = i + kWaves < t1;
+            const Place next = more ? place(i + kWaves) : p;
+            tile(std::false_type{}, p, next, more);
+            p = next;
+        }
+#pragma unroll 1
+        for (; i < t1; i += kWaves) {
+            const bool more = i + kWaves < t1;
+            const Place next = more ? place(i + kWaves) : p;
+            tile(std::true_type{}, p, next, more);
+            p = next;
+        }
+    }
+    if (any_odd) {
+        // Whatever its probability, a seen infinity makes its column infinite
+        // and a NaN makes it NaN: each is added as it is.
+#pragma unroll 1
+        for (int j = 0; j < a.T; ++j) {
+            const int p = len + j, at = prefix_tiles + p / kTile - t0;
+            if (at < 0 || at >= t1 - t0 || at % kWaves != wave) continue;   // another wave's tile
+            const uint16_t* const vp = a.v + (long long)page_of(a, own_table, p, len + a.T) * a.page_stride + (long long)(p & page_mask) * a.token_stride + head;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int d = 0; d < DT; d += 2) {
+                    const uint32_t v = *(const uint32_t*)(vp + DT * (4 * g + q) + d);
+                    const float lo = not_finite<BF16>(v) ? unpack1<BF16>(v & 0xffffu) : 0.f;
+                    const float up = not_finite<BF16>(v >> 16) ? unpack1<BF16>(v >> 16) : 0.f;
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const bool sees = (see[rt] >> j) & 1;
+                        o[rt][d][q] += sees ? lo : 0.f, o[rt][d + 1][q] += sees ? up : 0.f;
+                    }
+                }
+        }
+    }
+    // The waves' parts, each a sum with its own maximum, joined in wave order.
+    float* const ml = (float*)smem;                                          // [waves][kRows][2]
+    float* const os = (float*)(smem + kWaves * kRows * 2 * sizeof(float));   // [waves][kRows][D]
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        l[rt] = sum4(l[rt]);
+        if (g == 0) {
+            float* const at = ml + (wave * kRows + 16 * rt + c) * 2;
+            at[0] = m[rt], at[1] = l[rt];
+        }
+    }
+    __syncthreads();
+    const bool direct = a.parts == 1;
+    auto out_row = [&](uint32_t row) { return ((size_t)b * a.T + row / G) * a.Hq + kvh * G + row % G; };
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const uint32_t in_block = 16 * rt + c, row = row0 + in_block;
+        float top = m[rt], sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, ml[(w * kRows + in_block) * 2]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float* const at = ml + (w * kRows + in_block) * 2;
+            sum += weight_of(at[0], top) * at[1];
+        }
+        float f = weight_of(m[rt], top);
+        if (direct) f = sum == 0.f ? 0.f : f / sum;
+        if (wave == 0 && g == 0 && row < R) {
+            if (!direct) a.part_ml[out_row(row) * a.parts + a.SP + split] = float2{top, sum};
+            else if (a.lse) a.lse[out_row(row)] = sum == 0.f ? -__builtin_inff() : (top - kLift<BF16> + __builtin_log2f(sum)) * kLn2;
+        }
+        // Lane (c, g) holds columns DT (4 g + q) + d of its row.
+        float* const to = os + ((size_t)wave * kRows + in_block) * D;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int d = 0; d < DT; d += 4)
+                *(float4_t*)(to + DT * (4 * g + q) + d) = float4_t{o[rt][d][q] * f, o[rt][d + 1][q] * f, o[rt][d + 2][q] * f, o[rt][d + 3][q] * f};
+    }
+    __syncthreads();
+    for (int e = t * 4; e < kRows * D; e += kWaves * 256) {
+        const uint32_t row = row0 + e / D;
+        if (row >= R) break;
+        float4_t v = *(const float4_t*)(os + e);
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += *(const float4_t*)(os + (size_t)w * kRows * D + e);
+        if (direct)
+            *(u32x2_t*)(a.out + out_row(row) * D + e % D) = u32x2_t{pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3])};
+        else
+            *(float4_t*)(a.part_o + (out_row(row) * a.parts + a.SP + split) * D + e % D) = v;
+    }
+}
+
+// Scores, maxima, sums and O are fp32.  The probabilities are rounded to the
+// type of q, k and v, as the matrix unit takes them (the sum l adds them before
+// that): at most 2^-8 (bf16) or 2^-11 (f16) of each key's probability, averaged over the keys.
+template <bool BF16, int D, int RT>
+__global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void prefix_attn_kernel(PrefixArgs a) {
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+    // Consecutive workgroups go to the XCDs in turn: the blocks of rows that read the
+    // same keys sit 8 apart, on one XCD.  Groups of eight of the two kinds are mixed evenly.
+    const uint32_t group = blockIdx.x >> 3, x = blockIdx.x & 7, all = a.prefix_groups + a.own_groups;
+    const uint32_t own = (uint64_t)group * a.own_groups / all, after = (uint64_t)(group + 1) * a.own_groups / all;
+    if (after > own) {
+        const uint32_t id = own / (uint32_t)a.RO * 8 + x;
+        if (id < (uint32_t)a.B * a.Hkv * a.SO) own_work<BF16, D, RT>(a, id, own % (uint32_t)a.RO, smem);
+    } else {
+        const uint32_t i = group - own, unit = i / (uint32_t)a.RB * 8 + x;
+        if (unit < (uint32_t)a.Hkv * a.SP) prefix_work<BF16, D>(a, unit, i % (uint32_t)a.RB, smem);
+    }
+}
+
+// Joins a row's parts: o = sum 2^(m_s - top) o_s / sum 2^(m_s - top) l_s, in part order.
+// W waves per row: with four, wave w adds parts w, w + 4, .. and the four sums are added in wave order.
+template <bool BF16, int D, int W>
+__global__ __launch_bounds__(256) void prefix_merge_kernel(PrefixArgs a) {
+    constexpr int C = D / 64;   // columns per lane
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave % W;
+    const size_t row = (size_t)blockIdx.x * (4 / W) + wave / W, rows = (size_t)a.B * a.T * a.Hq;
+    const bool there = row < rows;
+    float v[C], sum = 0.f, top = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = 0.f;
+    if (there) {
+        const float* const src = a.part_o + row * a.parts * D + lane * C;
+        float2 ml = float2{-__builtin_inff(), 0.f};
+        if (lane < a.parts) ml = a.part_ml[row * a.parts + lane];
+        float x[8][C];
+        auto fetch = [&](int s0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int s = min(s0 + W * j, a.parts - 1);   // past the end: a part that is not added
+#pragma unroll
+                for (int i = 0; i < C; ++i) x[j][i] = src[(size_t)s * D + i];
+            }
+        };
+        fetch(w);
+        top = ml.x;
+#pragma unroll
+        for (int s = 32; s >= 1; s >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, s));
+        const float f = weight_of(ml.x, top);   // of part `lane`
+        sum = f * ml.y;
+#pragma unroll
+        for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s);
+        for (int s0 = w; s0 < a.parts; s0 += 8 * W) {
+            if (s0 != w) fetch(s0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int s = s0 + W * j;
+                const float fs = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(f), s & 63));
+#pragma unroll
+                for (int i = 0; i < C; ++i) v[i] = s < a.parts ? __builtin_fmaf(fs, x[j][i], v[i]) : v[i];
+            }
+        }
+    }
+    if constexpr (W > 1) {
+        __shared__ float parts[4][D];
+#pragma unroll
+        for (int i = 0; i < C; ++i) parts[wave][lane * C + i] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            v[i] = parts[0][lane * C + i];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) v[i] += parts[k][lane * C + i];
+        }
+    }
+    if (!there || w != 0) return;
+    const float f = sum == 0.f ? 0.f : 1.0f / sum;
+    uint16_t* const to = a.out + row * D + lane * C;
+    if constexpr (C == 1) {
+        *to = (uint16_t)pack2<BF16>(v[0] * f, 0.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; i += 2) *(uint32_t*)(to + i) = pack2<BF16>(v[i] * f, v[i + 1] * f);
+    }
+    if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -__builtin_inff() : (top - kLift<BF16> + __builtin_log2f(sum)) * kLn2;
+}
+
+typedef void (*kernel_t)(PrefixArgs);
+
+template <bool BF16, int D>
+kernel_t attend(int rt) {
+    return rt == 1 ? prefix_attn_kernel<BF16, D, 1> : prefix_attn_kernel<BF16, D, 2>;
+}
+template <bool BF16>
+kernel_t attend(int D, int rt) {
+    return D == 64 ? attend<BF16, 64>(rt) : D == 128 ? attend<BF16, 128>(rt) : attend<BF16, 256>(rt);
+}
+template <bool BF16, int D>
+kernel_t merge(int w) {
+    return w == 1 ? prefix_merge_kernel<BF16, D, 1> : prefix_merge_kernel<BF16, D, 4>;
+}
+template <bool BF16>
+kernel_t merge(int D, int w) {
+    return D == 64 ? merge<BF16, 64>(w) : D == 128 ? merge<BF16, 128>(w) : merge<BF16, 256>(w);
+}
+
+// The kernels' dynamic LDS passes the default limit: said once per process and device.
+void allow_lds() {
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices || done[dev].load(std::memory_order_acquire)) return;
+    for (int D : {64, 128, 256})
+        for (int rt : {1, 2})
+            for (kernel_t k : {attend<false>(D, rt), attend<true>(D, rt)})
+                (void)hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicLds);
+    done[dev].store(true, std::memory_order_release);
+}
+
+size_t lds_bytes(int D, int rt, bool shared) {
+    const size_t ring = shared ? (size_t)(D == 256 ? 2 : 4) * 2 * kTile * D * 2 : 0;
+    const size_t join = (size_t)kWaves * 16 * rt * (D + 2) * sizeof(float);
+    return ring > join ? ring : join;
+}
+
+struct Plan {
+    int SP, SO, RB, RO, rt;
+    int run;                  // requests of a launch
+    long long prefix_groups, own_groups;
+    size_t ws;
+    bool ok;
+};
+
+// The form and the splits of the keys with the least estimated time: workgroups
+// of both kinds fill the GPU's places, each a start and a number of steps.
+Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len) {
+    const double kStart = 5.0, kMerge = 4.0, kPartBytesPerUs = 4e6;
+    const double own_step = D == 64 ? 0.7 : D == 128 ? 1.2 : 1.6, prefix_step = D == 64 ? 0.6 : D == 128 ? 0.9 : 1.6;
+    const int G = Hq / Hkv, R = T * G;
+    const double places = (double)w4h::cu_count() * (D == 256 ? 1 : 2);
+    const long long ptiles = ((long long)max_prefix + kTile - 1) / kTile, otiles = ((long long)max_len + T + kTile - 1) / kTile;
+    Plan best{};
+    double least = 0;
+    for (int shared = 0; shared <= (max_prefix > 0 ? 1 : 0); ++shared) {
+        for (long long SP : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48}) {
+            if (!shared && SP > 1) break;
+            if (shared && SP > 1 && SP * 4 > ptiles) break;
+            for (long long SO : {1, 2, 3, 4, 6, 8, 12, 16, 32, 64}) {
+                Plan p{};
+                p.SP = shared ? (int)SP : 0, p.SO = (int)SO;
+                const long long tiles = otiles + (shared ? 0 : ptiles);
+                if (SO > 1 && SO * 2 * kWaves > tiles) break;
+                const int parts = p.SP + p.SO;
+                if (parts > kMaxParts) break;
+                p.rt = R <= 16 ? 1 : 2;
+                p.RO = (R + 16 * p.rt - 1) / (16 * p.rt);
+                // Requests of a run: their parts stay below the limit.
+                const long long row = parts > 1 ? (long long)T * Hq * parts * (D + 2) * 4 : 0;
+                if (row > (long long)kMaxPartBytes) break;
+                long long run = row ? (long long)kMaxPartBytes / row : B;
+                run = run < 1 ? 1 : run < B ? run : B;
+                const long long runs = (B + run - 1) / run;
+                p.run = (int)((B + runs - 1) / runs);
+                p.RB = (int)(((long long)p.run * R + kBlockRows - 1) / kBlockRows);
+                p.prefix_groups = ((long long)Hkv * p.SP + 7) / 8 * p.RB;
+                p.own_groups = ((long long)p.run * Hkv * SO + 7) / 8 * p.RO;
+                p.ws = parts > 1 ? w4h::ws_bytes((size_t)p.run * row) : 0;
+                const long long merge_rows = (long long)p.run * T * Hq;
+                if ((p.prefix_groups + p.own_groups) * 8 * 256 > kMaxLanes || (parts > 1 && merge_rows * 256 > kMaxLanes)) continue;
+                const double np = (double)Hkv * p.SP * p.RB, no = (double)p.run * Hkv * SO * p.RO;
+                const double dp = shared ? kStart + ceil((double)ptiles / SP) * prefix_step : 0;
+                const double dn = kStart + ceil((double)tiles / SO / kWaves) * own_step * p.rt;
+                const double longest = dp > dn ? dp : dn, work = (np * dp + no * dn) / places;
+                double time = work > longest ? work + 0.3 * longest : longest;
+                if (parts > 1) time += kMerge + (double)merge_rows * parts * D * 8 / kPartBytesPerUs;
+                time *= runs;
+                if (!best.ok || time < least) best = p, best.ok = true, least = time;
+            }
+        }
+    }
+    return best;
+}
+
+int check_shape(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len) {
+    if (B < 1 || T < 1 || T > 64 || Hkv < 1 || Hq < Hkv || Hq % Hkv || max_len < 0 || max_len > (1 << 30) || max_prefix < 0 ||
+        max_prefix > (1 << 30))
+        return W4A16_ERR_SHAPE;
+    if (Hq > (1 << 16) || (long long)B * Hq > (1LL << 24)) return W4A16_ERR_SHAPE;
+    if (D != 64 && D != 128 && D != 256) return W4A16_ERR_UNSUPPORTED;
+    return W4A16_OK;
+}
+
+}  // namespace
+
+extern "C" int prefix_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len,
+                                           size_t* bytes) {
+    if (!bytes) return W4A16_ERR_NULL;
+    if (int rc = check_shape(B, T, Hq, Hkv, D, max_prefix, max_len)) return rc;
+    const Plan p = make_plan(B, T, Hq, Hkv, D, max_prefix, max_len);
+    if (!p.ok) return W4A16_ERR_UNSUPPORTED;
+    *bytes = p.ws;
+    return W4A16_OK;
+}
+
+extern "C" int prefix_attn(const void* q, long long q_stride, const void* k, const void* v, int dtype, int num_pages,
+                           int page_size, long long page_stride, long long token_stride, long long head_stride,
+                           const int32_t* prefix_table, const int32_t* prefix_len, int max_prefix,
+                           const int32_t* block_table, int table_stride, const int32_t* lens, int max_len,
+                           const uint64_t* tree_mask, float scale, void* out, float* lse, int B, int T, int Hq, int Hkv,
+                           int D, void* workspace, size_t workspace_bytes, w4a16_stream_t stream) {
+    if (!q || !k || !v || !prefix_len || !block_table || !lens || !tree_mask || !out) return W4A16_ERR_NULL;
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_ERR_DTYPE;
+    if (int rc = check_shape(B, T, Hq, Hkv, D, max_prefix, max_len)) return rc;
+    if (max_prefix > 0 && !prefix_table) return W4A16_ERR_NULL;
+    if (num_pages < 1 || page_size < 1 || (page_size & (page_size - 1)) || table_stride < 1 ||
+        (long long)table_stride * page_size < (long long)max_len + T)
+        return W4A16_ERR_SHAPE;
+    if (q_stride < (long long)Hq * D || q_stride % 8 || page_stride < 0 || token_stride < 0 || head_stride < 0 ||
+        (unsigned long long)page_size * (unsigned long long)token_stride >= (1ull << 30) || page_stride % 8 ||
+        token_stride % 8 || head_stride % 8 || !(scale == scale) || scale - scale != 0.f)
+        return W4A16_ERR_SHAPE;
+    for (const void* p : {q, k, v, (const void*)out, (const void*)workspace})
+        if (!w4h::aligned16(p)) return W4A16_ERR_ALIGN;
+    if (((uintptr_t)prefix_table & 3) || ((uintptr_t)prefix_len & 3) || ((uintptr_t)lens & 3) || ((uintptr_t)block_table & 3) ||
+        ((uintptr_t)tree_mask & 7) || ((uintptr_t)lse & 3))
+        return W4A16_ERR_ALIGN;
+    if (page_size < 16) return W4A16_ERR_UNSUPPORTED;   // a half of a tile lies in one page
+    const Plan p = make_plan(B, T, Hq, Hkv, D, max_prefix, max_len);
+    if (!p.ok) return W4A16_ERR_UNSUPPORTED;
+    if (p.ws && !workspace) return W4A16_ERR_NULL;
+    if (workspace_bytes < p.ws) return W4A16_ERR_WORKSPACE;
+    PrefixArgs a{};
+    a.k = (const uint16_t*)k, a.v = (const uint16_t*)v;
+    a.prefix_table = prefix_table, a.prefix_len = prefix_len;
+    a.q_stride = q_stride, a.page_stride = page_stride, a.token_stride = token_stride, a.head_stride = head_stride;
+    a.num_pages = num_pages, a.table_stride = table_stride, a.max_prefix = max_prefix, a.max_len = max_len;
+    while ((1 << a.page_shift) < page_size) ++a.page_shift;
+    a.scale2 = fmaxf(fabsf(scale) * kLog2e, 0x1p-126f);   // not 0: -inf marks what a row does not see
+    a.q_sign = scale < 0.f ? 0x80008000u : 0u;
+    a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv;
+    a.SP = p.SP, a.SO = p.SO, a.RO = p.RO, a.parts = p.SP + p.SO;
+    const bool bf16 = dtype == W4A16_BF16;
+    const hipStream_t st = (hipStream_t)stream;
+    const size_t lds = lds_bytes(D, p.rt, p.SP > 0);
+    allow_lds();
+    w4h::begin_launches();
+    for (int b0 = 0; b0 < B; b0 += p.run) {
+        const size_t tok = (size_t)b0 * T;
+        a.B = B - b0 < p.run ? B - b0 : p.run;
+        a.RB = (int)(((long long)a.B * T * a.G + kBlockRows - 1) / kBlockRows);
+        a.prefix_groups = (uint32_t)(((long long)Hkv * p.SP + 7) / 8 * a.RB);
+        a.own_groups = (uint32_t)(((long long)a.B * Hkv * p.SO + 7) / 8 * a.RO);
+        a.q = (const uint16_t*)q + tok * q_stride, a.table = block_table + (size_t)b0 * table_stride;
+        a.lens = lens + b0, a.mask = tree_mask + tok;
+        a.out = (uint16_t*)out + tok * Hq * D, a.lse = lse ? lse + tok * Hq : nullptr;
+        const size_t rows = (size_t)a.B * T * Hq;
+        a.part_o = (float*)w4h::ws_part(workspace);
+        a.part_ml = workspace ? (float2*)(a.part_o + rows * a.parts * D) : nullptr;
+        hipLaunchKernelGGL(bf16 ? attend<true>(D, p.rt) : attend<false>(D, p.rt), dim3((a.prefix_groups + a.own_groups) * 8), dim3(kWaves * 64), lds,
+                           st, a);
+        if (a.parts > 1) {
+            const int w = rows * 4 < 16384 && a.parts > 8 ? 4 : 1;
+            hipLaunchKernelGGL(bf16 ? merge<true>(D, w) : merge<false>(D, w), dim3((unsigned)((rows * w + 3) / 4)), dim3(256), 0, st, a);
+        }
+    }
+    w4h::note_variant("%s D=%lld prefix_splits=%lld own_splits=%lld row_tiles=%lld requests=%lld of %lld", "prefix_attn", D, p.SP, p.SO, p.rt, p.run, B);
+    return w4h::launch_status();
+}
