@@ -45,7 +45,7 @@ extern "C" {
  *            largest element at most is left out for a 16-bit y, 2^-21 for an fp32 y).
  * The result is deterministic.  A row with a NaN or an infinity changes no other row.
  * Other than base = y nothing overlaps.
- * Shape: 1 <= M <= 2^26, N >= 8, N % 8 == 0, N <= 2^24, 8 <= K <= 2^20, K % 8 == 0, ldx < 2^26,
+ * Shape: 1 <= M <= 2^26, N >= 8, N % 8 == 0, N <= 2^24, 8 <= K <= 2^20, K % 8 == 0, ldx <= 2^24, ldy <= 2^25,
  * R a multiple of 8 up to 256, 1 <= n_adapters, 1 <= parts <= 4.  workspace may be NULL where the query
  * reports 0.  Both calls return W4A16_ERR_UNSUPPORTED where a launch would need 2^32 work-items. */
 int lora_workspace_bytes(int M, int N, int K, int R, int parts, size_t* bytes);

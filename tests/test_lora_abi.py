@@ -54,7 +54,7 @@ def test_refusals():
         assert call(**{p: GOOD + 2}) == -3, p
     assert call(dtype="f32") == -4 and call(dtype=9) == -4 and call(ydt=5) == -4
     for over in (dict(M=0), dict(M=(1 << 26) + 1), dict(N=0), dict(N=324), dict(N=(1 << 24) + 8), dict(K=0), dict(K=12), dict(K=(1 << 20) + 8),
-                 dict(R=0), dict(R=12), dict(R=264), dict(n=0), dict(ldx=504), dict(ldx=516), dict(ldx=1 << 26), dict(ldy=312), dict(ldy=324),
+                 dict(R=0), dict(R=12), dict(R=264), dict(n=0), dict(ldx=504), dict(ldx=516), dict(ldx=(1 << 24) + 8), dict(ldy=(1 << 25) + 8), dict(ldy=312), dict(ldy=324),
                  dict(cols=[128, 128]), dict(cols=[128, 64, 136]), dict(cols=[120, 72, 128]), dict(cols=[320, 0]), dict(cols=[64, -64, 320]),
                  dict(cols=[312]), dict(cols=[64, 64, 64, 64, 64]), dict(cols=[256, 64, 4, -4])):
         assert call(**over) == -2, over
@@ -79,9 +79,10 @@ def test_size_limits_are_the_same_for_the_query_and_the_call():
     # Launches of 2^32 work-items (calls in a process that sees no GPU: -7 is a launch that failed there).
     code = ("import ctypes, bit_weight_only_03_amd as L\n"
             "lib, b, p = L._lib_get(), ctypes.c_size_t(), 4096\n"
-            "for M, N, K, R in ((1 << 26, 1 << 24, 64, 16), (1 << 26, 1024, 1 << 20, 256), (1 << 26, 64, 64, 8), (1, 64, 64, 8)):\n"
-            "    print(lib.lora_workspace_bytes(M, N, K, R, 1, ctypes.byref(b)),\n"
-            "          lib.lora_add(p, 1, K, p, p, None, None, 1, p, None, p, 1, N, None, 1, M, N, K, R, p, 1 << 60, None))\n")
+            "for M, parts, K, R in ((1 << 26, 4, 64, 16), (1 << 26, 1, 1 << 20, 256), (1 << 26, 2, 64, 8), (1, 1, 64, 8)):\n"
+            "    N, cols = 256 * parts, (ctypes.c_int * parts)(*([256] * parts))\n"
+            "    print(lib.lora_workspace_bytes(M, N, K, R, parts, ctypes.byref(b)),\n"
+            "          lib.lora_add(p, 1, K, p, p, None, None, 1, p, None, p, 1, N, cols, parts, M, N, K, R, p, 1 << 60, None))\n")
     out = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, HIP_VISIBLE_DEVICES="-1"), capture_output=True, text=True,
                          timeout=300, cwd=ROOT)
     assert out.returncode == 0, out.stderr[-500:]
