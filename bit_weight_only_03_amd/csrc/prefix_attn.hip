@@ -11,9 +11,9 @@
 //
 // Products.  Scores are computed transposed, S^T = K Q^T, so that a lane holds one
 // row's scores, in the layout in which O^T = V^T P^T takes P as its B operand
-// once the slots of k are named after the keys that the lane holds.  V^T's
-// columns are free: lane r of operand tile t takes column (D/N) r + t, so it
-// reads consecutive columns of each key and pairs keys up with byte permutes.
+// once the slots of k are named after the keys that the lane holds.  V^T comes from
+// LDS by transposing reads (prefix work), or (own work) lane r of operand tile t takes column
+// (D/16) r + t, so that it loads consecutive columns of each key and pairs keys up with byte permutes.
 #include "attn_common.h"
 #include "../../include/prefix_attn.h"
 
@@ -24,6 +24,7 @@ namespace {
 constexpr int kTile = 32;              // keys per tile
 constexpr int kWaves = 4;
 constexpr int kBlockRows = 32 * kWaves;   // rows of a workgroup of prefix work
+constexpr int kStages = 4;             // ring stages of prefix work
 constexpr int kMaxParts = 64;
 constexpr size_t kMaxPartBytes = (size_t)128 << 20;
 
@@ -50,6 +51,7 @@ struct PrefixArgs {
     int SO, RO;        // own work: splits, blocks of rows
     int parts;         // SP + SO
     uint32_t prefix_groups, own_groups;   // groups of eight workgroups
+    int own_first;     // the own work's workgroups take longer
 };
 
 // Probabilities are 2^(x - m + kLift): in f16 that keeps them normal down to
@@ -63,6 +65,7 @@ template <bool BF16>
 constexpr float kSlack = BF16 ? 8.f : 3.f;
 
 typedef float float16_t __attribute__((ext_vector_type(16)));
+typedef short v4i16_t __attribute__((ext_vector_type(4)));
 
 template <bool BF16>
 __device__ __forceinline__ float16_t mfma32(const u32x4_t& a, const u32x4_t& b, const float16_t& c) {
@@ -90,6 +93,13 @@ __device__ __forceinline__ int page_of(const PrefixArgs& a, const int* table, in
     return min(max(((const_ptr_t)table)[min(p, end - 1) >> a.page_shift], 0), a.num_pages - 1);
 }
 
+// V's 64-byte pieces of a key change places with the key, so that the four keys that a
+// transposing read takes together lie on different banks.
+template <int D>
+__device__ __forceinline__ uint32_t v_swizzle(uint32_t key) {
+    return D == 64 ? (key >> 1) & 1 : key & 3;
+}
+
 // The first of n tiles that part i of s takes (the first n % s parts take one more).
 __device__ __forceinline__ int share(int n, int s, int i) {
     const int each = (uint32_t)n / (uint32_t)s;
@@ -101,7 +111,7 @@ __device__ __forceinline__ int share(int n, int s, int i) {
 // Workgroup (unit, rb): keys [tile t0, tile t1) of the prefix for kv head unit / SP, rows rb * 128 .. of the B T G.
 template <bool BF16, int D>
 __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, uint32_t rb, uint8_t* smem) {
-    constexpr int NS = D == 256 ? 2 : 4;       // ring stages
+    constexpr int NS = kStages;
     constexpr int NT = D / 32;                 // operand tiles of O^T
     constexpr int KS = D / 16;                 // products per score tile
     constexpr int kChunks = D / 8;             // 16-byte chunks of a key
@@ -120,6 +130,7 @@ __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, 
     const int page_mask = (1 << a.page_shift) - 1;
     const uint32_t page_bytes = (uint32_t)page_mask * key_bytes + D * 2;
     const int key_in = lane / kChunks, pos = lane % kChunks;
+    const bool once = a.RB == 1;   // nobody else reads these keys
 
     const uint32_t rows = (uint32_t)a.B * a.T * a.G, row0 = rb * kBlockRows + wave * 32, G = a.G;
     const uint32_t row = min(row0 + c, rows - 1);      // past the rows: the last one again, not stored
@@ -140,9 +151,14 @@ __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, 
         const __amdgpu_buffer_rsrc_t rk = make_rsrc(a.k + at, page_bytes), rv = make_rsrc(a.v + at, page_bytes);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const uint32_t key = key_in + i * kKeys, k_off = 16u * (pos ^ ((wave * kSpan + key) & kSwz));
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr_t)(to + i * 1024), 16, key * key_bytes + k_off, in_page, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr_t)(to + kHalf + i * 1024), 16, key * key_bytes + 16u * pos, in_page, 0, 0);
+            const uint32_t key = key_in + i * kKeys, k_off = 16u * (pos ^ ((wave * kSpan + key) & kSwz)), v_off = 16u * (pos ^ (4 * v_swizzle<D>(key)));
+            if (once) {
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr_t)(to + i * 1024), 16, key * key_bytes + k_off, in_page, 0, kAuxNT);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr_t)(to + kHalf + i * 1024), 16, key * key_bytes + v_off, in_page, 0, kAuxNT);
+            } else {
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr_t)(to + i * 1024), 16, key * key_bytes + k_off, in_page, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr_t)(to + kHalf + i * 1024), 16, key * key_bytes + v_off, in_page, 0, 0);
+            }
         }
     };
     float16_t o[NT];
@@ -166,18 +182,45 @@ __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, 
 #pragma unroll
     for (int s = 0; s < KS; ++s) qf[s] ^= a.q_sign;
 
-    // One tile: scores, probabilities, product with V.  Score i of lane (c, hi) is
-    // that of key 8 (i / 4) + 4 hi + i % 4.  EDGE: some of its keys are past the end.
-    auto tile = [&](auto edge, const uint8_t* kt, const uint8_t* vt, int first) {
+    // K of a tile: the scores' A operand.
+    u32x4_t kf[KS];
+    auto read_k = [&](const uint8_t* kt) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kf[s] = *(const u32x4_t*)(kt + c * D * 2 + 16 * ((2 * s + hi) ^ (c & kSwz)));
+    };
+    // V^T of a tile: lane (c, hi) of operand tile d and half h has column 32 d + c of keys 16 h + 8 j + 4 hi + i
+    // (word 2 j + i / 2).  A transposing read of 16 lanes takes 16 columns of four keys: lane l asks
+    // for columns 4 (l % 4) .. of key l / 4 and gets column l of the four.
+    u32x4_t va[2][NT];
+    const uint32_t v_key = 4 * hi + ((lane & 15) >> 2), v_lane = v_key * D * 2 + 64 * v_swizzle<D>(v_key) + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+    auto read_v = [&](const uint8_t* vt) {
+        typedef __attribute__((address_space(3))) v4i16_t* tr_ptr_t;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int d = 0; d < NT; ++d)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const u32x2_t v = bitcast<u32x2_t>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr_t)(vt + (v_lane ^ (64 * d)) + (16 * h + 8 * j) * D * 2)));
+                    va[h][d][2 * j] = v[0], va[h][d][2 * j + 1] = v[1];
+                }
+    };
+    // One tile, whose K is in registers: scores, probabilities, product with V.  Score i of lane
+    // (c, hi) is that of key 8 (i / 4) + 4 hi + i % 4.  V is read beside the softmax, the next
+    // tile's K (after the barrier that says it has arrived) beside the product with V.
+    // Products go before the other wave's softmax (priorities: 414 -> 404 us for 1024 x 40 rows over 16384 keys).
+    // EDGE: some of its keys are past the end.
+    auto tile = [&](auto edge, const uint8_t* vt, int first, auto turn) {
         constexpr bool EDGE = decltype(edge)::value;
         float16_t x;
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = 0.f;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const u32x4_t kf = *(const u32x4_t*)(kt + c * D * 2 + 16 * ((2 * s + hi) ^ (c & kSwz)));
-            x = mfma32<BF16>(kf, qf[s], x);
-        }
+        for (int s = 0; s < KS; ++s) x = mfma32<BF16>(kf[s], qf[s], x);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        read_v(vt);
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (EDGE) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = first + 8 * (i >> 2) + 4 * hi + (i & 3) < P ? x[i] : -__builtin_inff();
@@ -203,51 +246,56 @@ __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, 
             sum += x[i];
         }
         l += sum;   // this lane's keys; the two lanes of a row are added at the end
+        u32x4_t pf[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u32x4_t pf;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) pf[j] = pack2<BF16>(x[8 * h + 2 * j], x[8 * h + 2 * j + 1]);
-            constexpr int VW = NT / 2;   // dwords of a key per lane
-            uint32_t vr[8][VW];
+            for (int j = 0; j < 4; ++j) pf[h][j] = pack2<BF16>(x[8 * h + 2 * j], x[8 * h + 2 * j + 1]);
+        __builtin_amdgcn_s_setprio(1);
+        wait_loads<63>();   // V has arrived: its place in the ring may be loaded anew after the barrier
+        turn();
+        if constexpr (EDGE) {   // 0 times what lies past the end could be NaN
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int key = 16 * h + 8 * (j >> 2) + 4 * hi + (j & 3);
-                const uint8_t* const p = vt + key * D * 2 + c * VW * 4;
-                if constexpr (VW == 1) {
-                    vr[j][0] = *(const uint32_t*)p;
-                } else if constexpr (VW == 2) {
-                    const u32x2_t v = *(const u32x2_t*)p;
-                    vr[j][0] = v[0], vr[j][1] = v[1];
-                } else {
-                    const u32x4_t v = *(const u32x4_t*)p;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) vr[j][e] = v[e];
+                for (int w = 0; w < 4; ++w) {
+                    const int left = P - first - (16 * h + 8 * (w >> 1) + 4 * hi + 2 * (w & 1));   // keys of the word that are there
+                    const uint32_t keep = left >= 2 ? ~0u : left == 1 ? 0xffffu : 0u;
+#pragma unroll
+                    for (int d = 0; d < NT; ++d) va[h][d][w] &= keep;
                 }
-                if constexpr (EDGE) {   // 0 times what lies past the end could be NaN
-#pragma unroll
-                    for (int w = 0; w < VW; ++w) vr[j][w] = first + key < P ? vr[j][w] : 0u;
-                }
-            }
-#pragma unroll
-            for (int d = 0; d < NT; ++d) {
-                u32x4_t va;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    va[j] = __builtin_amdgcn_perm(vr[2 * j + 1][d >> 1], vr[2 * j][d >> 1], d & 1 ? 0x07060302u : 0x05040100u);
-                o[d] = mfma32<BF16>(va, pf, o[d]);
-            }
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int d = 0; d < NT; ++d) o[d] = mfma32<BF16>(va[h][d], pf[h], o[d]);
+        __builtin_amdgcn_sched_barrier(0);
     };
-    auto step = [&](auto edge, int n) {
-        wait_loads<(NS - 2) * 2 * kPer>();
+    auto slot = [&](int n) { return smem + (n - t0) % NS * kStage; };
+    // Tile n + 1 has arrived for everybody, and nobody needs tile n - 1's place any more.
+    auto arrive = [&](int n) {
+        wait_loads<(NS - 3) * 2 * kPer>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         issue(n + NS - 1, next);
         next = look_up(n + NS);
-        if (row0 >= rows) return;   // a wave without rows only loads
-        const uint8_t* const kt = smem + (n - t0) % NS * kStage;
-        tile(edge, kt, kt + kHalf, n * kTile);
+    };
+    const bool idle = row0 >= rows;   // a wave without rows only loads
+    if (t0 < t1) {
+        wait_loads<(NS - 2) * 2 * kPer>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (!idle) read_k(slot(t0));
+    }
+    auto step = [&](auto edge, int n) {
+        if (idle) {
+            arrive(n);
+            return;
+        }
+        tile(edge, slot(n) + kHalf, n * kTile, [&] {
+            arrive(n);
+            read_k(slot(n + 1));   // past the last tile: the last one again
+        });
     };
     int n = t0;
     for (const int plain = min(t1, P / kTile); n < plain; ++n) step(std::false_type{}, n);
@@ -257,18 +305,12 @@ __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, 
     l = sum2(l);
     const size_t part = out_row * a.parts + split;
     if (hi == 0) a.part_ml[part] = float2{m, l};
-    // o[d][i] is column NT (8 (i / 4) + 4 hi + i % 4) + d.
-    float* const to = a.part_o + part * D;
+    // o[d][i] is column 32 d + 8 (i / 4) + 4 hi + i % 4.
+    float* const to = a.part_o + part * D + 4 * hi;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float* const p = to + NT * (8 * (i >> 2) + 4 * hi + (i & 3));
-        if constexpr (NT == 2) {
-            *(float2*)p = float2{o[0][i], o[1][i]};
-        } else {
+    for (int d = 0; d < NT; ++d)
 #pragma unroll
-            for (int d = 0; d < NT; d += 4) *(float4_t*)(p + d) = float4_t{o[d][i], o[d + 1][i], o[d + 2][i], o[d + 3][i]};
-        }
-    }
+        for (int i = 0; i < 16; i += 4) *(float4_t*)(to + 32 * d + 2 * i) = float4_t{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
 }
 
 // ---------------------------------------------------------------- own work
@@ -503,7 +545,8 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
     }
     // The waves' parts, each a sum with its own maximum, joined in wave order.
     float* const ml = (float*)smem;                                          // [waves][kRows][2]
-    float* const os = (float*)(smem + kWaves * kRows * 2 * sizeof(float));   // [waves][kRows][D]
+    constexpr int kPitch = D + 4;                                            // rows side by side in the lanes: not on the same banks
+    float* const os = (float*)(smem + kWaves * kRows * 2 * sizeof(float));   // [waves][kRows][kPitch]
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         l[rt] = sum4(l[rt]);
@@ -533,7 +576,7 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
             else if (a.lse) a.lse[out_row(row)] = sum == 0.f ? -__builtin_inff() : (top - kLift<BF16> + __builtin_log2f(sum)) * kLn2;
         }
         // Lane (c, g) holds columns DT (4 g + q) + d of its row.
-        float* const to = os + ((size_t)wave * kRows + in_block) * D;
+        float* const to = os + ((size_t)wave * kRows + in_block) * kPitch;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -544,9 +587,10 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
     for (int e = t * 4; e < kRows * D; e += kWaves * 256) {
         const uint32_t row = row0 + e / D;
         if (row >= R) break;
-        float4_t v = *(const float4_t*)(os + e);
+        const float* const from = os + (e / D) * kPitch + e % D;
+        float4_t v = *(const float4_t*)from;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += *(const float4_t*)(os + (size_t)w * kRows * D + e);
+        for (int w = 1; w < kWaves; ++w) v += *(const float4_t*)(from + (size_t)w * kRows * kPitch);
         if (direct)
             *(u32x2_t*)(a.out + out_row(row) * D + e % D) = u32x2_t{pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3])};
         else
@@ -561,14 +605,14 @@ template <bool BF16, int D, int RT>
 __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) void prefix_attn_kernel(PrefixArgs a) {
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     // Consecutive workgroups go to the XCDs in turn: the blocks of rows that read the
-    // same keys sit 8 apart, on one XCD.  Groups of eight of the two kinds are mixed evenly.
-    const uint32_t group = blockIdx.x >> 3, x = blockIdx.x & 7, all = a.prefix_groups + a.own_groups;
-    const uint32_t own = (uint64_t)group * a.own_groups / all, after = (uint64_t)(group + 1) * a.own_groups / all;
-    if (after > own) {
-        const uint32_t id = own / (uint32_t)a.RO * 8 + x;
-        if (id < (uint32_t)a.B * a.Hkv * a.SO) own_work<BF16, D, RT>(a, id, own % (uint32_t)a.RO, smem);
+    // same keys sit 8 apart, on one XCD.  The kind whose workgroups take longer comes first.
+    const uint32_t group = blockIdx.x >> 3, x = blockIdx.x & 7;
+    const uint32_t before = a.own_first ? a.own_groups : a.prefix_groups, i = group < before ? group : group - before;
+    if ((group < before) == (a.own_first != 0)) {
+        const uint32_t id = i / (uint32_t)a.RO * 8 + x;
+        if (id < (uint32_t)a.B * a.Hkv * a.SO) own_work<BF16, D, RT>(a, id, i % (uint32_t)a.RO, smem);
     } else {
-        const uint32_t i = group - own, unit = i / (uint32_t)a.RB * 8 + x;
+        const uint32_t unit = i / (uint32_t)a.RB * 8 + x;
         if (unit < (uint32_t)a.Hkv * a.SP) prefix_work<BF16, D>(a, unit, i % (uint32_t)a.RB, smem);
     }
 }
@@ -672,8 +716,8 @@ void allow_lds() {
 }
 
 size_t lds_bytes(int D, int rt, bool shared) {
-    const size_t ring = shared ? (size_t)(D == 256 ? 2 : 4) * 2 * kTile * D * 2 : 0;
-    const size_t join = (size_t)kWaves * 16 * rt * (D + 2) * sizeof(float);
+    const size_t ring = shared ? (size_t)kStages * 2 * kTile * D * 2 : 0;
+    const size_t join = (size_t)kWaves * 16 * rt * (D + 6) * sizeof(float);
     return ring > join ? ring : join;
 }
 
@@ -681,36 +725,39 @@ struct Plan {
     int SP, SO, RB, RO, rt;
     int run;                  // requests of a launch
     long long prefix_groups, own_groups;
+    bool own_first;
     size_t ws;
     bool ok;
 };
 
 // The form and the splits of the keys with the least estimated time: workgroups
-// of both kinds fill the GPU's places, each a start and a number of steps.
+// of both kinds fill the GPU's places, each a start and a number of steps (measured on
+// MI355X, a workgroup beside another one on its CU), the longer kind first; and no less than the bytes take.
 Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len) {
-    const double kStart = 5.0, kMerge = 4.0, kPartBytesPerUs = 4e6;
-    const double own_step = D == 64 ? 0.7 : D == 128 ? 1.2 : 1.6, prefix_step = D == 64 ? 0.6 : D == 128 ? 0.9 : 1.6;
+    const double kStart = 4.0, kMerge = 4.0, kBytesPerUs = 5.5e6, kPartBytesPerUs = 4.5e6;
+    const double own_step = D == 64 ? 0.9 : D == 128 ? 2.2 : 3.5, prefix_step = D == 64 ? 0.7 : D == 128 ? 1.15 : 1.6;
     const int G = Hq / Hkv, R = T * G;
-    const double places = (double)w4h::cu_count() * (D == 256 ? 1 : 2);
+    const long long places = (long long)w4h::cu_count() * (D == 256 ? 1 : 2);
     const long long ptiles = ((long long)max_prefix + kTile - 1) / kTile, otiles = ((long long)max_len + T + kTile - 1) / kTile;
     Plan best{};
     double least = 0;
     for (int shared = 0; shared <= (max_prefix > 0 ? 1 : 0); ++shared) {
-        for (long long SP : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48}) {
-            if (!shared && SP > 1) break;
-            if (shared && SP > 1 && SP * 4 > ptiles) break;
-            for (long long SO : {1, 2, 3, 4, 6, 8, 12, 16, 32, 64}) {
+        const int rt = R <= 16 ? 1 : 2, RO = (R + 16 * rt - 1) / (16 * rt);
+        const long long units = (long long)B * Hkv * RO, blocks = (long long)Hkv * (((long long)B * R + kBlockRows - 1) / kBlockRows);
+        // Splits worth a look: a few, and those that fill the places once, or what the other kind leaves of them.
+        const long long left = places > units ? (places - units) / blocks : 0;
+        for (long long SP : {1LL, 2LL, 3LL, 4LL, 6LL, 8LL, 12LL, 16LL, 24LL, 32LL, 48LL, places / blocks, left}) {
+            if (!shared && SP != 1) continue;
+            if (shared && (SP < 1 || SP >= kMaxParts || (SP > 1 && SP * 4 > ptiles))) continue;
+            for (long long SO : {1LL, 2LL, 3LL, 4LL, 6LL, 8LL, 12LL, 16LL, 32LL, 64LL, places / units}) {
                 Plan p{};
-                p.SP = shared ? (int)SP : 0, p.SO = (int)SO;
+                p.SP = shared ? (int)SP : 0, p.SO = (int)SO, p.rt = rt, p.RO = RO;
                 const long long tiles = otiles + (shared ? 0 : ptiles);
-                if (SO > 1 && SO * 2 * kWaves > tiles) break;
                 const int parts = p.SP + p.SO;
-                if (parts > kMaxParts) break;
-                p.rt = R <= 16 ? 1 : 2;
-                p.RO = (R + 16 * p.rt - 1) / (16 * p.rt);
+                if (SO < 1 || parts > kMaxParts || (SO > 1 && SO * 2 * kWaves > tiles)) continue;
                 // Requests of a run: their parts stay below the limit.
                 const long long row = parts > 1 ? (long long)T * Hq * parts * (D + 2) * 4 : 0;
-                if (row > (long long)kMaxPartBytes) break;
+                if (row > (long long)kMaxPartBytes) continue;
                 long long run = row ? (long long)kMaxPartBytes / row : B;
                 run = run < 1 ? 1 : run < B ? run : B;
                 const long long runs = (B + run - 1) / run;
@@ -723,10 +770,15 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len
                 if ((p.prefix_groups + p.own_groups) * 8 * 256 > kMaxLanes || (parts > 1 && merge_rows * 256 > kMaxLanes)) continue;
                 const double np = (double)Hkv * p.SP * p.RB, no = (double)p.run * Hkv * SO * p.RO;
                 const double dp = shared ? kStart + ceil((double)ptiles / SP) * prefix_step : 0;
-                const double dn = kStart + ceil((double)tiles / SO / kWaves) * own_step * p.rt;
-                const double longest = dp > dn ? dp : dn, work = (np * dp + no * dn) / places;
-                double time = work > longest ? work + 0.3 * longest : longest;
-                if (parts > 1) time += kMerge + (double)merge_rows * parts * D * 8 / kPartBytesPerUs;
+                const double turns = (double)tiles / SO / kWaves, dn = kStart + 0.5 * (turns + ceil(turns)) * own_step * p.rt;
+                p.own_first = dn > dp;
+                // The longer kind in whole rounds, the shorter one in the places that are left.
+                const double nl = p.own_first ? no : np, dl = p.own_first ? dn : dp, work = (np * dp + no * dn) / places;
+                const double rounds = ceil(nl / places) * dl;
+                double time = work > rounds ? work + 0.25 * (p.own_first ? dp : dn) : rounds;
+                const double bytes = ((shared ? (double)ptiles : (double)ptiles * 0.1 * p.run) + (double)otiles * p.run) * kTile * Hkv * D * 4;
+                if (time < bytes / kBytesPerUs) time = bytes / kBytesPerUs + 0.1 * dl;
+                if (parts > 1) time += kMerge + (double)merge_rows * parts * D * 4 / kPartBytesPerUs;
                 time *= runs;
                 if (!best.ok || time < least) best = p, best.ok = true, least = time;
             }
@@ -792,7 +844,7 @@ extern "C" int prefix_attn(const void* q, long long q_stride, const void* k, con
     a.scale2 = fmaxf(fabsf(scale) * kLog2e, 0x1p-126f);   // not 0: -inf marks what a row does not see
     a.q_sign = scale < 0.f ? 0x80008000u : 0u;
     a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv;
-    a.SP = p.SP, a.SO = p.SO, a.RO = p.RO, a.parts = p.SP + p.SO;
+    a.SP = p.SP, a.SO = p.SO, a.RO = p.RO, a.parts = p.SP + p.SO, a.own_first = p.own_first;
     const bool bf16 = dtype == W4A16_BF16;
     const hipStream_t st = (hipStream_t)stream;
     const size_t lds = lds_bytes(D, p.rt, p.SP > 0);
@@ -813,7 +865,8 @@ extern "C" int prefix_attn(const void* q, long long q_stride, const void* k, con
         hipLaunchKernelGGL(bf16 ? attend<true>(D, p.rt) : attend<false>(D, p.rt), dim3((a.prefix_groups + a.own_groups) * 8), dim3(kWaves * 64), lds,
                            st, a);
         if (a.parts > 1) {
-            const int w = rows * 4 < 16384 && a.parts > 8 ? 4 : 1;
+            // Four waves join a row where few rows have many parts (320 of 57: 4.8 us, a wave each 6.8; 3584 of 13: 7.8 and 6.7).
+            const int w = rows * 4 < 16384 && a.parts > 16 ? 4 : 1;
             hipLaunchKernelGGL(bf16 ? merge<true>(D, w) : merge<false>(D, w), dim3((unsigned)((rows * w + 3) / 4)), dim3(256), 0, st, a);
         }
     }
