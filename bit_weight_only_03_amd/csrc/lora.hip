@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kRows = 16;              // rows of a tile
 constexpr int kMaxR = 256;
-constexpr int kMaxWaves = 8;
 constexpr int kGroup = 128;            // columns that a wave takes at a time
 constexpr int kUnit = 64;              // k that a wave takes at a time: a line of each row
 constexpr int kStep = 32;              // ranks of B at a time
@@ -249,8 +248,8 @@ __device__ __forceinline__ void each_adapter(const LoraArgs& a, int tile, int tu
 // workgroups, a multiple of eight), whose adapters then stay in its L2.
 __device__ __forceinline__ uint32_t run_of_rows(uint32_t i, uint32_t n) { return i % 8 * (n / 8) + i / 8; }
 
-// Stages of the second product's ring, 8 KiB each, for each of four waves.
-constexpr int second_stages(bool one) { return one ? 2 : 3; }
+// Stages of the second product's ring, 8 KiB each, for each of four waves (three leave no room for a second workgroup on the CU).
+constexpr int kSecondStages = 2;
 
 // y of columns [n0, n1) of a tile's rows, Y its type.  make_h() leaves s h in hb (and back); the first
 // loads are on their way meanwhile.  Rows and columns that are not there are past
@@ -349,18 +348,24 @@ struct Second {
         for (int i = 0; i < 4; ++i) f[i] = BF16 ? 1.f : back[4 * g + i];
     }
 
-    // At most 32 ranks, a group or two for a wave: b straight to registers, asked for before h is made.
+    // At most 32 RS ranks, a group or two for a wave: b straight to registers, asked for before h is made.
+    template <int RS>
     struct Few {
-        u32x4_t w[8], base[4][kWords];
+        u32x4_t w[RS][8], base[4][kWords];
     };
-    __device__ __forceinline__ void few_load(Few& q, int n) const {
+    template <int RS>
+    __device__ __forceinline__ void few_load(Few<RS>& q, int n) const {
         const __amdgpu_buffer_rsrc_t rb = columns(n);
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-            q.w[t] = bitcast<u32x4_t>(__builtin_amdgcn_raw_buffer_load_b128(rb, 8 * g < r.rank ? (8 * c + t) * row_bytes + 16 * g : kNowhere, 0, 0));
+        for (int s = 0; s < RS; ++s)
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                q.w[s][t] = bitcast<u32x4_t>(
+                    __builtin_amdgcn_raw_buffer_load_b128(rb, kStep * s + 8 * g < r.rank ? (8 * c + t) * row_bytes + 64 * s + 16 * g : kNowhere, 0, 0));
         load_base(q.base, n);
     }
-    __device__ __forceinline__ void few(Few& q, const uint16_t* hb, int stride, const float* back) const {
+    template <int RS>
+    __device__ __forceinline__ void few(Few<RS>& q, const uint16_t* hb, int stride, const float* back) const {
         float f[4];
         scales(back, f);
 #pragma unroll 1
@@ -369,7 +374,8 @@ struct Second {
             float4_t acc[8];
 #pragma unroll
             for (int t = 0; t < 8; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
-            multiply(q.w, hb, stride, 0, acc);
+#pragma unroll
+            for (int s = 0; s < RS; ++s) multiply(q.w[s], hb, stride, s, acc);
             result(acc, q.base, f, out);
             __builtin_amdgcn_sched_barrier(0);
             few_load(q, n + step);
@@ -380,7 +386,7 @@ struct Second {
     // At most 32 ranks: a ring of groups, and as many bases in registers.
     template <typename F>
     __device__ __forceinline__ void one_step(uint8_t* ring, const uint16_t* hb, int stride, const float* back, F make_h) const {
-        constexpr int D = second_stages(true);
+        constexpr int D = kSecondStages;
         u32x4_t base[D][4][kWords], out[4][kWords];
         int n = n0 + kGroup * wave;
 #pragma unroll
@@ -421,7 +427,7 @@ struct Second {
     // More ranks: a ring of steps of 32.
     template <typename F>
     __device__ __forceinline__ void steps(uint8_t* ring, const uint16_t* hb, int stride, const float* back, F make_h) const {
-        constexpr int D = second_stages(false);
+        constexpr int D = kSecondStages;
         const int steps = max((r.rank + kStep - 1) / kStep, 1);
         int n = n0 + kGroup * wave, ahead_n = n, ahead_s = 0, slot = 0;
         auto next = [&] {   // asks for the step after the last one that was asked for
@@ -462,13 +468,14 @@ struct Second {
 
 // One launch: both products, a workgroup for (tile, turn, column block); the first product is
 // made again by each block of columns, from L2.
+constexpr int both_waves(int rk) { return rk > 2 ? 4 : 8; }
 template <bool BF16, int RK, int Y>
-__global__ __launch_bounds__(kMaxWaves * 64, 2) void lora_both_kernel(LoraArgs a) {
-    constexpr int NT = BF16 && Y == W4A16_F32 ? 3 : 2, stride = kStep + 8;
+__global__ __launch_bounds__(both_waves(RK) * 64, 2) void lora_both_kernel(LoraArgs a) {
+    constexpr int NT = BF16 && Y == W4A16_F32 ? 3 : 2, RS = RK > 2 ? 2 : 1, stride = kStep * RS + 8;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     uint8_t* const ring = smem;
-    float* const hf = (float*)(smem + first_lds(RK, 1, kMaxWaves));   // [16][R + 4]
-    float* const back = hf + kRows * (kStep + 4);                     // [16]
+    float* const hf = (float*)(smem + first_lds(RK, 1, both_waves(RK)));   // [16][R + 4]
+    float* const back = hf + kRows * (kStep * RS + 4);                     // [16]
     uint16_t* const hb = (uint16_t*)(back + kRows);                   // [NT][16][stride]
     const int blocks = a.block_start[a.parts], block = blockIdx.x % (uint32_t)blocks;
     const uint32_t unit = blockIdx.x / (uint32_t)blocks;
@@ -479,7 +486,7 @@ __global__ __launch_bounds__(kMaxWaves * 64, 2) void lora_both_kernel(LoraArgs a
     // base copied for rows without an adapter, unless it is y itself
     each_adapter<kRows>(a, tile, turn, a.turns, a.base != a.y, [&](const Rows& r) {
         const Second<BF16, NT, Y> second(a, r, n0, n1);
-        typename Second<BF16, NT, Y>::Few q;
+        typename Second<BF16, NT, Y>::template Few<RS> q;
         second.few_load(q, n0 + kGroup * second.wave);
         sum_h<BF16, RK, 1>(a, r, part * a.R, part * a.R + r.rank, 0, units, ring, [&](int row, int j, const float4_t& v) {
             *(float4_t*)(hf + row * (a.R + 4) + j - part * a.R) = v;
@@ -507,14 +514,14 @@ __global__ __launch_bounds__(MT == 1 ? 512 : 256, 2) void lora_first_kernel(Lora
     });
 }
 
-// .. and their sums in slice order times B: few rows, or many of high rank.  RS: ranks in steps of 32.
+// .. and their sums in slice order times B: at most 64 rows, or more than 64 ranks.  RS: ranks in steps of 32.
 template <bool BF16, int Y, int RS>
 __global__ __launch_bounds__(256, 2) void lora_second_kernel(LoraArgs a) {
     constexpr int NT = BF16 && Y == W4A16_F32 ? 3 : 2, stride = kStep * RS + 8;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int t = threadIdx.x, ranks = a.parts * a.R;
-    uint8_t* const ring = smem + (t >> 6) * second_stages(RS == 1) * kStepBytes;
-    float* const hf = (float*)(smem + 4 * second_stages(RS == 1) * kStepBytes);   // [16][R + 4]
+    uint8_t* const ring = smem + (t >> 6) * kSecondStages * kStepBytes;
+    float* const hf = (float*)(smem + 4 * kSecondStages * kStepBytes);   // [16][R + 4]
     float* const back = hf + kRows * (kStep * RS + 4);                            // [16]
     uint16_t* const hb = (uint16_t*)(back + kRows);                               // [NT][16][stride]
     const uint32_t blocks = a.block_start[a.parts], unit = blockIdx.x / blocks;
@@ -553,9 +560,9 @@ __global__ __launch_bounds__(256, 2) void lora_second_kernel(LoraArgs a) {
     });
 }
 
-// The same of many rows, up to 64 ranks: a workgroup takes 512 columns of a run of row
-// tiles.  It makes h of the whole run first; then a wave keeps its 128 columns of b in
-// registers for as long as the adapter stays the same, and only base and y move.
+// The same of more than 64 rows, up to 64 ranks: a workgroup takes 512 columns of a run of row tiles, and every turns-th
+// of each tile's adapters.  It makes h of the whole run first; then a wave keeps its 128 columns of
+// b in registers for as long as the adapter stays the same, and only base and y move.
 template <bool BF16, int Y, int RS>
 __global__ __launch_bounds__(256, 2) void lora_rows_kernel(LoraArgs a) {
     constexpr int NT = BF16 && Y == W4A16_F32 ? 3 : 2, stride = kStep * RS + 8, D = 2;
@@ -565,8 +572,8 @@ __global__ __launch_bounds__(256, 2) void lora_rows_kernel(LoraArgs a) {
     float* const back = (float*)(ids + a.run * kRows);      // [run 16]
     uint16_t* const hb = (uint16_t*)(back + a.run * kRows); // [run][NT][16][stride]
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), c = lane & 15, g = lane >> 4;
-    const uint32_t blocks = a.block_start[a.parts], id = run_of_rows(blockIdx.x, gridDim.x);
-    const int block = id % blocks, first = id / blocks * a.run, tiles = min(a.run, (a.M + kRows - 1) / kRows - first);
+    const uint32_t each = gridDim.x / (uint32_t)a.turns, id = run_of_rows(blockIdx.x % each, each), blocks = a.block_start[a.parts];
+    const int turn = blockIdx.x / each, block = id % blocks, first = id / blocks * a.run, tiles = min(a.run, (a.M + kRows - 1) / kRows - first);
     if (tiles <= 0) return;
     int part = 0;
     while (part + 1 < a.parts && block >= a.block_start[part + 1]) ++part;
@@ -684,10 +691,11 @@ __global__ __launch_bounds__(256, 2) void lora_rows_kernel(LoraArgs a) {
             };
             float4_t acc[8];
             uint64_t left = __builtin_amdgcn_ballot_w64(mine >= 0);
-            while (left) {
+            for (int nth = 0; left; ++nth) {
                 const int one = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
                 const uint64_t same = __builtin_amdgcn_ballot_w64(mine == one);
                 left &= ~same;
+                if (nth % a.turns != turn) continue;
                 if (one != held) take(one);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) acc[k] = float4_t{0.f, 0.f, 0.f, 0.f};
@@ -696,7 +704,7 @@ __global__ __launch_bounds__(256, 2) void lora_rows_kernel(LoraArgs a) {
                 put(acc, (uint32_t)same);
             }
             const uint64_t none = __builtin_amdgcn_ballot_w64(mine == -1);
-            if (none && a.base != a.y) {   // base copied
+            if (none && turn == 0 && a.base != a.y) {   // base copied
 #pragma unroll
                 for (int k = 0; k < 8; ++k) acc[k] = float4_t{0.f, 0.f, 0.f, 0.f};
                 put(acc, (uint32_t)none);
@@ -711,7 +719,7 @@ typedef void (*kernel_t)(LoraArgs);
 // The kernels by type and sizes.
 template <bool BF16, int Y>
 kernel_t both(int R) {
-    return R <= 16 ? lora_both_kernel<BF16, 1, Y> : lora_both_kernel<BF16, 2, Y>;
+    return R <= 16 ? lora_both_kernel<BF16, 1, Y> : R <= 32 ? lora_both_kernel<BF16, 2, Y> : lora_both_kernel<BF16, 4, Y>;
 }
 template <bool BF16, int Y>
 kernel_t second(int rs) {
@@ -755,7 +763,7 @@ void allow_lds() {
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices || done[dev].load(std::memory_order_acquire)) return;
     auto allow = [](kernel_t k) { (void)hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicLds); };
     for (int y : {W4A16_F16, W4A16_BF16, W4A16_F32}) {
-        for (int R : {16, 32}) allow(both<false>(R, y)), allow(both<true>(R, y));
+        for (int R : {16, 32, 64}) allow(both<false>(R, y)), allow(both<true>(R, y));
         for (int rs : {1, 2, 4, 8}) allow(second<false>(rs, y)), allow(second<true>(rs, y));
         for (int rs : {1, 2}) allow(rows<false>(rs, y)), allow(rows<true>(rs, y));
     }
@@ -776,34 +784,38 @@ struct Plan {
 Plan make_plan(int M, int N, int K, int R, int parts) {
     Plan p{};
     const long long cus = w4h::cu_count(), k_units = (K + kUnit - 1) / kUnit;
-    const bool many = M > 512;                           // few rows: a workgroup for each adapter that a tile may have
-    auto turns = [&](int rows) { return M < rows ? M : rows; };
+    const bool many = M > 512;
     p.tiles = (M + kRows - 1) / kRows;
-    p.turns = many ? 1 : turns(kRows);
-    const long long units = many ? p.tiles : M;          // (tile, adapter) pairs at most, or about
-    p.split = M > 64 || (long long)R * K > 100000 || R > kStep;
-    p.threads = p.split ? 256 : 512;
     p.rs = R <= 32 ? 1 : R <= 64 ? 2 : R <= 128 ? 4 : 8;
-    p.mt = many ? 4 : 1;
+    // One launch where a workgroup's read of a (R K x 2 bytes) costs less than a second launch, for one tile of rows: its LDS fills a CU.
+    p.split = M > kRows || (long long)R * K > 100000 || p.rs > 2;
     const int rows = p.split ? parts * R : R;            // of a that a workgroup multiplies
-    p.rk = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 ? 3 : 4;
-    // Columns of a block: a group for each wave; of few rows, enough blocks for two workgroups per CU.
-    const long long least = 4 * kGroup, want = (2 * cus + units - 1) / units;
-    long long cols = many && p.rs <= 2 ? least : (N + want - 1) / want;
-    cols = (cols + kGroup - 1) / kGroup * kGroup;
-    p.cols = (int)(cols < least ? least : cols);
+    p.rk = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 && p.split ? 3 : 4;
+    p.mt = many ? 4 : 1;
+    p.threads = p.split ? 256 : 64 * both_waves(p.rk);
+    const long long least = 4 * kGroup;                  // columns of a block: a group for each of four waves at least
     p.slices = 1;
-    if (many && p.rs <= 2) {
-        // Tiles of a run: the fewest with which all workgroups are on the GPU at once, two per CU.
-        const long long blocks = (N + p.cols - 1) / p.cols + parts - 1, places = 2 * cus / blocks, most = p.rs == 1 ? 16 : 8;
-        const long long run = places ? (p.tiles + places - 1) / places : most;
+    if (p.split && M > 64 && p.rs <= 2) {
+        // By runs of row tiles, the fewest with which all workgroups are on the GPU at once, two per
+        // CU; where one-tile runs leave places, several workgroups share a tile's adapters.
+        p.cols = (int)least;
+        const long long blocks = (N + least - 1) / least + parts - 1, places = 2 * cus / blocks, most = p.rs == 1 ? 16 : 8;
+        const long long run = places ? (p.tiles + places - 1) / places : most, share = places / p.tiles, one = M < kRows ? M : kRows;
         p.run = (int)(run < most ? run : most);
+        p.turns = (int)(share < 1 || many ? 1 : share < one ? share : one);
+    } else {
+        // A workgroup for each adapter that a tile may have (more than 64 rows are as often a few
+        // prompts': a quarter of them, the others looped over), and column blocks for two workgroups per CU.
+        const int one = M < kRows ? M : M <= 64 ? kRows : kRows / 4;
+        p.turns = many ? 1 : one;
+        const long long units = M <= 64 ? M : p.tiles, want = (2 * cus + units - 1) / units, cols = ((N + want - 1) / want + kGroup - 1) / kGroup * kGroup;
+        p.cols = (int)(cols < least ? least : cols);
     }
     if (p.split) {
         p.first_threads = p.mt > 1 ? 256 : 512;
         p.first_tiles = (M + kRows * p.mt - 1) / (kRows * p.mt);
-        p.first_turns = many ? 1 : turns(kRows);
-        const long long first = many ? p.first_tiles : M, waves = p.first_threads / 64;
+        p.first_turns = many ? 1 : M < kRows ? M : M <= 64 ? kRows : kRows / 4;
+        const long long first = M <= 64 ? M : many ? p.first_tiles : 2 * p.first_tiles, waves = p.first_threads / 64;
         long long s = cus / first;                       // a workgroup fills a CU's LDS
         s = s < k_units / (2 * waves) ? s : k_units / (2 * waves);         // two units for each wave at least
         s = s < 16 ? s : 16;
@@ -824,7 +836,7 @@ long long first_blocks(const Plan& p) {
     return p.split ? (p.mt > 1 ? (each + 7) / 8 * 8 : each) * p.first_turns : 0;
 }
 long long second_blocks(const Plan& p, long long blocks) {
-    return p.run ? ((p.tiles + p.run - 1) / p.run * blocks + 7) / 8 * 8 : p.tiles * p.turns * blocks;
+    return p.turns * (p.run ? ((p.tiles + p.run - 1) / p.run * blocks + 7) / 8 * 8 : p.tiles * blocks);
 }
 
 int check_shape(int M, int N, int K, int R, int parts) {
@@ -888,7 +900,7 @@ extern "C" int lora_add(const void* x, int dtype, long long ldx, const void* a, 
     const int terms = bf16 && y_dtype == W4A16_F32 ? 3 : 2;
     const hipStream_t st = (hipStream_t)stream;
     const size_t lds = p.run ? run_bytes(p.run, p.rs, terms)
-                             : (p.split ? 4 * second_stages(p.rs == 1) * (size_t)kStepBytes : first_lds(p.rk, 1, kMaxWaves)) + h_bytes(p.rs, terms);
+                             : (p.split ? 4 * kSecondStages * (size_t)kStepBytes : first_lds(p.rk, 1, both_waves(p.rk))) + h_bytes(p.rs, terms);
     allow_lds();
     w4h::begin_launches();
     if (p.split) {

@@ -182,44 +182,52 @@ __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, 
 #pragma unroll
     for (int s = 0; s < KS; ++s) qf[s] ^= a.q_sign;
 
-    // K of a tile: the scores' A operand.
-    u32x4_t kf[KS];
-    auto read_k = [&](const uint8_t* kt) {
+    // K of a tile: the scores' A operand.  Heads of 256 leave no registers for reading it (and
+    // all of V) ahead: they read pieces when they are needed.
+    constexpr bool kAhead = D < 256;
+    constexpr int KP = kAhead ? KS : 8;
+    u32x4_t kf[KP];
+    auto read_k = [&](const uint8_t* kt, int s0) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) kf[s] = *(const u32x4_t*)(kt + c * D * 2 + 16 * ((2 * s + hi) ^ (c & kSwz)));
+        for (int i = 0; i < KP; ++i) {
+            const int s = s0 + i;
+            kf[i] = *(const u32x4_t*)(kt + c * D * 2 + 16 * ((2 * s + hi) ^ (c & kSwz)));
+        }
     };
     // V^T of a tile: lane (c, hi) of operand tile d and half h has column 32 d + c of keys 16 h + 8 j + 4 hi + i
     // (word 2 j + i / 2).  A transposing read of 16 lanes takes 16 columns of four keys: lane l asks
     // for columns 4 (l % 4) .. of key l / 4 and gets column l of the four.
-    u32x4_t va[2][NT];
+    u32x4_t va[kAhead ? 2 : 1][NT];
     const uint32_t v_key = 4 * hi + ((lane & 15) >> 2), v_lane = v_key * D * 2 + 64 * v_swizzle<D>(v_key) + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
-    auto read_v = [&](const uint8_t* vt) {
+    auto read_v = [&](const uint8_t* vt, int h) {
         typedef __attribute__((address_space(3))) v4i16_t* tr_ptr_t;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int d = 0; d < NT; ++d)
 #pragma unroll
-            for (int d = 0; d < NT; ++d)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const u32x2_t v = bitcast<u32x2_t>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr_t)(vt + (v_lane ^ (64 * d)) + (16 * h + 8 * j) * D * 2)));
-                    va[h][d][2 * j] = v[0], va[h][d][2 * j + 1] = v[1];
-                }
+            for (int j = 0; j < 2; ++j) {
+                const u32x2_t v = bitcast<u32x2_t>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_ptr_t)(vt + (v_lane ^ (64 * d)) + (16 * h + 8 * j) * D * 2)));
+                va[kAhead ? h : 0][d][2 * j] = v[0], va[kAhead ? h : 0][d][2 * j + 1] = v[1];
+            }
     };
     // One tile, whose K is in registers: scores, probabilities, product with V.  Score i of lane
     // (c, hi) is that of key 8 (i / 4) + 4 hi + i % 4.  V is read beside the softmax, the next
     // tile's K (after the barrier that says it has arrived) beside the product with V.
     // Products go before the other wave's softmax (priorities: 414 -> 404 us for 1024 x 40 rows over 16384 keys).
-    // EDGE: some of its keys are past the end.
-    auto tile = [&](auto edge, const uint8_t* vt, int first, auto turn) {
-        constexpr bool EDGE = decltype(edge)::value;
+    // EDGE: some of its keys are past the end (a copy of its own: behind branches, whole tiles take 4 % longer).
+    auto tile = [&](auto is_edge, const uint8_t* kt, const uint8_t* vt, int first, auto turn) {
+        constexpr bool EDGE = decltype(is_edge)::value;
         float16_t x;
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = 0.f;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) x = mfma32<BF16>(kf[s], qf[s], x);
+        for (int s = 0; s < KS; ++s) {
+            if (!kAhead && s % KP == 0) read_k(kt, s);
+            x = mfma32<BF16>(kf[s % KP], qf[s], x);
+        }
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
-        read_v(vt);
+        read_v(vt, 0);
+        if constexpr (kAhead) read_v(vt, 1);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (EDGE) {
 #pragma unroll
@@ -252,24 +260,28 @@ __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, 
 #pragma unroll
             for (int j = 0; j < 4; ++j) pf[h][j] = pack2<BF16>(x[8 * h + 2 * j], x[8 * h + 2 * j + 1]);
         __builtin_amdgcn_s_setprio(1);
-        wait_loads<63>();   // V has arrived: its place in the ring may be loaded anew after the barrier
-        turn();
-        if constexpr (EDGE) {   // 0 times what lies past the end could be NaN
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
+        auto multiply = [&](int h) {
+            if constexpr (EDGE) {   // 0 times what lies past the end could be NaN
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int left = P - first - (16 * h + 8 * (w >> 1) + 4 * hi + 2 * (w & 1));   // keys of the word that are there
                     const uint32_t keep = left >= 2 ? ~0u : left == 1 ? 0xffffu : 0u;
 #pragma unroll
-                    for (int d = 0; d < NT; ++d) va[h][d][w] &= keep;
+                    for (int d = 0; d < NT; ++d) va[kAhead ? h : 0][d][w] &= keep;
                 }
+            }
+#pragma unroll
+            for (int d = 0; d < NT; ++d) o[d] = mfma32<BF16>(va[kAhead ? h : 0][d], pf[h], o[d]);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if constexpr (!kAhead) {
+            multiply(0);
+            read_v(vt, 1);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int d = 0; d < NT; ++d) o[d] = mfma32<BF16>(va[h][d], pf[h], o[d]);
-        __builtin_amdgcn_sched_barrier(0);
+        wait_loads<63>();   // V has arrived: its place in the ring may be loaded anew after the barrier
+        turn();
+        if constexpr (kAhead) multiply(0);
+        multiply(1);
     };
     auto slot = [&](int n) { return smem + (n - t0) % NS * kStage; };
     // Tile n + 1 has arrived for everybody, and nobody needs tile n - 1's place any more.
@@ -285,16 +297,16 @@ __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, 
         wait_loads<(NS - 2) * 2 * kPer>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        if (!idle) read_k(slot(t0));
+        if (kAhead && !idle) read_k(slot(t0), 0);
     }
-    auto step = [&](auto edge, int n) {
+    auto step = [&](auto is_edge, int n) {
         if (idle) {
             arrive(n);
             return;
         }
-        tile(edge, slot(n) + kHalf, n * kTile, [&] {
+        tile(is_edge, slot(n), slot(n) + kHalf, n * kTile, [&] {
             arrive(n);
-            read_k(slot(n + 1));   // past the last tile: the last one again
+            if constexpr (kAhead) read_k(slot(n + 1), 0);   // past the last tile: the last one again
         });
     };
     int n = t0;
@@ -363,14 +375,10 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
         long long at[2];        // elements from the cache's start to the halves' pages
         uint32_t in_page[2];    // bytes
     };
-    // In order: the tiles of nothing but prefix, of nothing but context, the prefix's
-    // last one where it ends inside, and the request's with its end and the drafts.
-    const int prefix_whole = P / kTile, whole = prefix_whole + len / kTile, prefix_rest = prefix_tiles - prefix_whole;
     auto place = [&](int i) {
         Place p;
-        const bool shared = i < prefix_whole || (prefix_rest && i == whole);
-        const int own = i - (i < whole ? prefix_whole : prefix_tiles);
-        p.first = (shared ? min(i, prefix_whole) : own) * kTile;
+        const bool shared = i < prefix_tiles;
+        p.first = (shared ? i : i - prefix_tiles) * kTile;
         p.len = shared ? P : len, p.T = shared ? 0 : a.T;
         const int* const table = shared ? a.prefix_table : own_table;
 #pragma unroll
@@ -412,9 +420,10 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
         }
     };
     // One tile; its keys are in registers, its values and the next tile's keys on their way.
-    // EDGE: some of its keys are drafts or past the end.
-    auto tile = [&](auto edge, const Place& p, const Place& next, bool more) {
-        constexpr bool EDGE = decltype(edge)::value;
+    // What drafts and the end need stands behind branches: a second copy of this code would have to
+    // be fetched, which a short call waits for (8 requests of 7 drafts, heads of 256: 10.0 -> 7.1 us).
+    auto tile = [&](const Place& p, const Place& next, bool more) {
+        const bool edge = p.first + kTile > p.len;   // some of its keys are drafts or past the end
         float4_t sc[2][RT];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -432,7 +441,7 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][rt][i & 3];
-            if constexpr (EDGE) {
+            if (edge) {
                 const uint32_t bits = visible(p.T ? see[rt] : 0, d0) >> (4 * g);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -462,7 +471,7 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
 #pragma unroll
             for (int j = 0; j < 4; ++j) pf[rt][j] = pack2<BF16>(x[2 * j], x[2 * j + 1]);
         }
-        if constexpr (EDGE) {
+        if (edge) {
             // Keys past the end count as zeros.  A draft's infinity or NaN must not
             // reach the rows that do not see it (0 * inf): it is taken out of the
             // product, and given to the rows that do after the loop.
@@ -506,17 +515,10 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
         load_k(p);
         load_v(p);
 #pragma unroll 1
-        for (; i < min(t1, whole); i += kWaves) {
-            const bool more = i + kWaves < t1;
-            const Place next = more ? place(i + kWaves) : p;
-            tile(std::false_type{}, p, next, more);
-            p = next;
-        }
-#pragma unroll 1
         for (; i < t1; i += kWaves) {
             const bool more = i + kWaves < t1;
             const Place next = more ? place(i + kWaves) : p;
-            tile(std::true_type{}, p, next, more);
+            tile(p, next, more);
             p = next;
         }
     }
@@ -692,7 +694,7 @@ kernel_t attend(int rt) {
 }
 template <bool BF16>
 kernel_t attend(int D, int rt) {
-    return D == 64 ? attend<BF16, 64>(rt) : D == 128 ? attend<BF16, 128>(rt) : attend<BF16, 256>(rt);
+    return D == 64 ? attend<BF16, 64>(rt) : D == 128 ? attend<BF16, 128>(rt) : prefix_attn_kernel<BF16, 256, 1>;
 }
 template <bool BF16, int D>
 kernel_t merge(int w) {
@@ -742,7 +744,7 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len
     Plan best{};
     double least = 0;
     for (int shared = 0; shared <= (max_prefix > 0 ? 1 : 0); ++shared) {
-        const int rt = R <= 16 ? 1 : 2, RO = (R + 16 * rt - 1) / (16 * rt);
+        const int rt = R <= 16 || D == 256 ? 1 : 2, RO = (R + 16 * rt - 1) / (16 * rt);
         const long long units = (long long)B * Hkv * RO, blocks = (long long)Hkv * (((long long)B * R + kBlockRows - 1) / kBlockRows);
         // Splits worth a look: a few, and those that fill the places once, or what the other kind leaves of them.
         const long long left = places > units ? (places - units) / blocks : 0;

@@ -79,7 +79,7 @@ def test_size_limits_are_the_same_for_the_query_and_the_call():
     # Launches of 2^32 work-items (calls in a process that sees no GPU: -7 is a launch that failed there).
     code = ("import ctypes, bit_weight_only_03_amd as L\n"
             "lib, b, p = L._lib_get(), ctypes.c_size_t(), 4096\n"
-            "for M, parts, K, R in ((1 << 26, 4, 64, 16), (1 << 26, 1, 1 << 20, 256), (1 << 26, 2, 64, 8), (1, 1, 64, 8)):\n"
+            "for M, parts, K, R in ((1 << 26, 4, 64, 128), (1 << 26, 1, 1 << 20, 256), (1 << 26, 2, 64, 8), (1, 1, 64, 8)):\n"
             "    N, cols = 256 * parts, (ctypes.c_int * parts)(*([256] * parts))\n"
             "    print(lib.lora_workspace_bytes(M, N, K, R, parts, ctypes.byref(b)),\n"
             "          lib.lora_add(p, 1, K, p, p, None, None, 1, p, None, p, 1, N, cols, parts, M, N, K, R, p, 1 << 60, None))\n")
