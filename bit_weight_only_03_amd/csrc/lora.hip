@@ -47,6 +47,7 @@ struct LoraArgs {
     int cols;             // columns of a block, a multiple of 64
     int turns, first_turns;   // workgroups that share a tile's adapters
     uint32_t first_tiles; // row tiles of the first launch, which may be larger
+    int first_groups;     // of 16 RK rows of a
     int run;              // row tiles of a workgroup of the second launch of many rows
     int slices;           // slices of K (1 where the products are one launch)
 };
@@ -497,18 +498,19 @@ __global__ __launch_bounds__(both_waves(RK) * 64, 2) void lora_both_kernel(LoraA
     });
 }
 
-// Two launches, where that costs more: slices of the sums over K, of all parts ..
+// Two launches, where that costs more: slices of the sums over K, 16 RK rows of the parts' a each ..
 template <bool BF16, int RK, int MT>
 __global__ __launch_bounds__(MT == 1 ? 512 : 256, 2) void lora_first_kernel(LoraArgs a) {
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const uint32_t each = gridDim.x / (uint32_t)a.first_turns, turn = blockIdx.x / each, at = blockIdx.x % each;
-    const uint32_t id = MT > 1 ? run_of_rows(at, each) : at, tile = id / (uint32_t)a.slices;
-    const int slice = id % (uint32_t)a.slices, units = (a.K + kUnit - 1) / kUnit, ranks = a.parts * a.R;
+    const uint32_t id = MT > 1 ? run_of_rows(at, each) : at, tile = id / (uint32_t)(a.slices * a.first_groups);
+    const int slice = id % (uint32_t)a.slices, group = id / (uint32_t)a.slices % (uint32_t)a.first_groups, units = (a.K + kUnit - 1) / kUnit, ranks = a.parts * a.R;
     if (tile >= a.first_tiles) return;
+    const int j0 = 16 * RK * group, j1 = min(j0 + 16 * RK, ranks);
     const int u0 = units * slice / a.slices, u1 = units * (slice + 1) / a.slices;
     each_adapter<kRows * MT>(a, tile, turn, a.first_turns, false, [&](const Rows& r) {
         float* const dst = a.h + ((size_t)slice * a.M + r.m0) * ranks;
-        sum_h<BF16, RK, MT>(a, r, 0, ranks, u0, u1, smem, [&](int row, int j, const float4_t& v) {
+        sum_h<BF16, RK, MT>(a, r, j0, j1, u0, u1, smem, [&](int row, int j, const float4_t& v) {
             if ((r.members >> row) & 1u && (int)((uint32_t)j % (uint32_t)a.R) < r.rank) *(float4_t*)(dst + (size_t)row * ranks + j) = v;
         });
     });
@@ -775,7 +777,7 @@ void allow_lds() {
 struct Plan {
     bool split;           // two launches
     int rk, mt, rs;       // the kernels' template arguments
-    int first_threads, threads, turns, first_turns, cols, slices;
+    int first_threads, threads, turns, first_turns, first_groups, cols, slices;
     int run;              // row tiles of a workgroup of the second launch; 0: not by runs
     long long tiles, first_tiles;
     size_t ws;
@@ -814,9 +816,10 @@ Plan make_plan(int M, int N, int K, int R, int parts) {
     if (p.split) {
         p.first_threads = p.mt > 1 ? 256 : 512;
         p.first_tiles = (M + kRows * p.mt - 1) / (kRows * p.mt);
+        p.first_groups = (rows + 16 * p.rk - 1) / (16 * p.rk);
         p.first_turns = many ? 1 : M < kRows ? M : M <= 64 ? kRows : kRows / 4;
         const long long first = M <= 64 ? M : many ? p.first_tiles : 2 * p.first_tiles, waves = p.first_threads / 64;
-        long long s = cus / first;                       // a workgroup fills a CU's LDS
+        long long s = cus / (first * p.first_groups);                       // a workgroup fills a CU's LDS
         s = s < k_units / (2 * waves) ? s : k_units / (2 * waves);         // two units for each wave at least
         s = s < 16 ? s : 16;
         p.slices = (int)(s < 1 ? 1 : s);
@@ -832,7 +835,7 @@ size_t run_bytes(int run, int rs, int terms) { return (size_t)run * kRows * (8 +
 
 // Workgroups of the launches.
 long long first_blocks(const Plan& p) {
-    const long long each = p.first_tiles * p.slices;
+    const long long each = p.first_tiles * p.first_groups * p.slices;
     return p.split ? (p.mt > 1 ? (each + 7) / 8 * 8 : each) * p.first_turns : 0;
 }
 long long second_blocks(const Plan& p, long long blocks) {
@@ -891,7 +894,7 @@ extern "C" int lora_add(const void* x, int dtype, long long ldx, const void* a, 
     g.ldx = ldx, g.ldy = ldy, g.y_dtype = y_dtype;
     g.n = n_adapters, g.M = M, g.N = N, g.K = K, g.R = R, g.parts = parts;
     g.cols = p.cols, g.turns = p.turns, g.first_turns = p.first_turns, g.slices = p.slices;
-    g.first_tiles = (uint32_t)p.first_tiles, g.run = p.run;
+    g.first_tiles = (uint32_t)p.first_tiles, g.first_groups = p.first_groups, g.run = p.run;
     for (int i = 0; i < parts; ++i) {
         const int cols = g.part_start[i + 1] - g.part_start[i];
         g.block_start[i + 1] = g.block_start[i] + (cols + p.cols - 1) / p.cols;

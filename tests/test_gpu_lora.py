@@ -108,6 +108,15 @@ CASES = [
     (530, 256, [136], 16, 7, "bf16", "bf16", "own", dict(y_pad=8)),                        # a workgroup takes all adapters of a tile
     (600, 2048, [192, 64], 104, 3, "f16", "f32", "in place", dict(ranks=[104, 50, 8])),
     (1100, 136, [64, 1000], 8, 4, "f16", "f16", "own", dict(ids=[i // 300 - 1 for i in range(1100)], scales=False)),
+    (2, 4000, [128, 128, 64], 64, 2, "bf16", "bf16", "own", {}),                           # rows of a by three workgroups
+    (70, 2000, [576], 128, 4, "f16", "f16", "own", dict(ranks=[128, 64, 7, 96])),
+    (200, 328, [264], 64, 6, "bf16", "bf16", "own", dict(ranks=[64, 40, 33, 32, 8, 0])),   # a tile's adapters over several workgroups
+    (65, 72, [8], 8, 20, "f16", "f32", "in place", {}),
+    (520, 1000, [16384, 64], 32, 40, "bf16", "bf16", "own", dict(ids=[i // 5 % 41 - 1 for i in range(520)])),
+    (700, 96, [512, 136], 48, 5, "f16", "f32", "in place", dict(ranks=[48, 41, 16, 5, 33])),
+    (4100, 64, [2048, 520], 16, 3, "bf16", "bf16", "own", {}),                             # runs of row tiles, several adapters in each
+    (3003, 72, [2048, 1032], 64, 4, "bf16", "f32", "own", dict(ids=[i // 100 % 5 - 1 for i in range(3003)])),
+    (1300, 40, [1024], 256, 3, "bf16", "bf16", "none", dict(ranks=[256, 200, 65])),
 ]
 
 
