@@ -25,7 +25,7 @@ constexpr int kTile = 32;              // keys per tile
 constexpr int kWaves = 4;
 constexpr int kBlockRows = 32 * kWaves;   // rows of a workgroup of prefix work
 constexpr int kStages = 4;             // ring stages of prefix work
-constexpr int kMaxParts = 64;
+constexpr int kMaxParts = 256;
 constexpr size_t kMaxPartBytes = (size_t)128 << 20;
 
 struct PrefixArgs {
@@ -632,8 +632,13 @@ __global__ __launch_bounds__(256) void prefix_merge_kernel(PrefixArgs a) {
     for (int i = 0; i < C; ++i) v[i] = 0.f;
     if (there) {
         const float* const src = a.part_o + row * a.parts * D + lane * C;
-        float2 ml = float2{-__builtin_inff(), 0.f};
-        if (lane < a.parts) ml = a.part_ml[row * a.parts + lane];
+        constexpr int H = kMaxParts / 64;   // a lane's parts: lane, lane + 64, ..
+        float2 ml[H];
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            ml[k] = float2{-__builtin_inff(), 0.f};
+            if (lane + 64 * k < a.parts) ml[k] = a.part_ml[row * a.parts + lane + 64 * k];
+        }
         float x[8][C];
         auto fetch = [&](int s0) {
 #pragma unroll
@@ -644,19 +649,25 @@ __global__ __launch_bounds__(256) void prefix_merge_kernel(PrefixArgs a) {
             }
         };
         fetch(w);
-        top = ml.x;
+#pragma unroll
+        for (int k = 0; k < H; ++k) top = __builtin_fmaxf(top, ml[k].x);
 #pragma unroll
         for (int s = 32; s >= 1; s >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, s));
-        const float f = weight_of(ml.x, top);   // of part `lane`
-        sum = f * ml.y;
+        float f[H];
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < H; ++k) f[k] = weight_of(ml[k].x, top), sum += f[k] * ml[k].y;
 #pragma unroll
         for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s);
         for (int s0 = w; s0 < a.parts; s0 += 8 * W) {
             if (s0 != w) fetch(s0);
+            float fh = f[0];   // the eight parts lie in one of the blocks of 64
+#pragma unroll
+            for (int k = 1; k < H; ++k) fh = s0 >= 64 * k ? f[k] : fh;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int s = s0 + W * j;
-                const float fs = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(f), s & 63));
+                const float fs = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(fh), s & 63));
 #pragma unroll
                 for (int i = 0; i < C; ++i) v[i] = s < a.parts ? __builtin_fmaf(fs, x[j][i], v[i]) : v[i];
             }
@@ -741,6 +752,7 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len
     const int G = Hq / Hkv, R = T * G;
     const long long places = (long long)w4h::cu_count() * (D == 256 ? 1 : 2);
     const long long ptiles = ((long long)max_prefix + kTile - 1) / kTile, otiles = ((long long)max_len + T + kTile - 1) / kTile;
+    const bool in_l2 = ptiles * kTile * Hkv * D * 4 <= (32LL << 20);
     Plan best{};
     double least = 0;
     for (int shared = 0; shared <= (max_prefix > 0 ? 1 : 0); ++shared) {
@@ -748,10 +760,12 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len
         const long long units = (long long)B * Hkv * RO, blocks = (long long)Hkv * (((long long)B * R + kBlockRows - 1) / kBlockRows);
         // Splits worth a look: a few, and those that fill the places once, or what the other kind leaves of them.
         const long long left = places > units ? (places - units) / blocks : 0;
-        for (long long SP : {1LL, 2LL, 3LL, 4LL, 6LL, 8LL, 12LL, 16LL, 24LL, 32LL, 48LL, places / blocks, left}) {
+        for (long long SP : {1LL, 2LL, 3LL, 4LL, 6LL, 8LL, 12LL, 16LL, 24LL, 32LL, 48LL, 64LL, 96LL, 128LL, 192LL, places / blocks, left}) {
             if (!shared && SP != 1) continue;
+            if (SP > 48 && SP * blocks > places) continue;   // many parts only where they fill the places once
             if (shared && (SP < 1 || SP >= kMaxParts || (SP > 1 && SP * 4 > ptiles))) continue;
-            for (long long SO : {1LL, 2LL, 3LL, 4LL, 6LL, 8LL, 12LL, 16LL, 32LL, 64LL, places / units}) {
+            for (long long SO : {1LL, 2LL, 3LL, 4LL, 6LL, 8LL, 12LL, 16LL, 32LL, 64LL, 128LL, places / units}) {
+                if (SO > 64 && SO * units > places) continue;
                 Plan p{};
                 p.SP = shared ? (int)SP : 0, p.SO = (int)SO, p.rt = rt, p.RO = RO;
                 const long long tiles = otiles + (shared ? 0 : ptiles);
@@ -778,7 +792,8 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len
                 const double nl = p.own_first ? no : np, dl = p.own_first ? dn : dp, work = (np * dp + no * dn) / places;
                 const double rounds = ceil(nl / places) * dl;
                 double time = work > rounds ? work + 0.25 * (p.own_first ? dp : dn) : rounds;
-                const double bytes = ((shared ? (double)ptiles : (double)ptiles * 0.1 * p.run) + (double)otiles * p.run) * kTile * Hkv * D * 4;
+                const double again = 1 + (p.run - 1) * (in_l2 ? 0.1 : 0.8);   // readings of a prefix that is not shared
+                const double bytes = ((double)ptiles * (shared ? 1 : again) + (double)otiles * p.run) * kTile * Hkv * D * 4;
                 if (time < bytes / kBytesPerUs) time = bytes / kBytesPerUs + 0.1 * dl;
                 if (parts > 1) time += kMerge + (double)merge_rows * parts * D * 4 / kPartBytesPerUs;
                 time *= runs;

@@ -339,3 +339,19 @@ def test_equals_the_tree_attention_without_a_prefix():
     L.tree_attn(c.g["q"], Hq * D, c.g["k"], c.g["v"], "f16", c.pages, page, ps, ts, hs, whole, whole.numel(),
                 torch.tensor([P + n], dtype=torch.int32, device=DEV), P + n, c.g["mask"], c.scale, out, None, 1, T, Hq, Hkv, D, work, work.numel())
     c.check(out)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "f16"), (128, "bf16"), (256, "bf16")])
+@pytest.mark.parametrize("P,lens", [(52003, [5, 40, 0]), (0, [70000]), (17, [66001, 3])])
+def test_more_than_64_parts(D, dtype, P, lens):
+    # One key/value head over a long axis: as many parts of the keys as the GPU has room for.
+    c = Case(len(lens), 2, 2, 1, D, 64, dtype, P, lens, seed=D)
+    out, lse = c.run()
+    c.check(out, lse)
+    sp, so = (int(f.split("=")[1]) for f in L.w4a16_last_variant().split()[2:4])
+    assert sp + so > 64 or D == 256, (sp, so)
+    # A prefix far shorter than its bound leaves most parts without a key.
+    if P > 70:
+        c.P, c.prefix, c.g["plen"][0] = 70, [t[:70] for t in c.prefix], 70
+        out, lse = c.run(max_prefix=P)
+        c.check(out, lse)
