@@ -14,6 +14,11 @@
 // that, an instruction takes 32 accesses of the CU's cache for 1 KiB instead of 16 or less.  So A,
 // B and the x of many rows go through LDS, whole lines at a time, in a ring that each wave
 // has for itself: no barriers, only counted waits.
+//
+// Few rows are bound by latency (one token through qkv 5120 -> 7168, rank 16: 7.9 us in a graph; what it
+// reads takes 0.2) and by reading the adapters (64 requests of 48 adapters through gate/up 5120 ->
+// 34816, ranks 8 to 32: 34.9 us, 2.0 TB/s of 69 MB, and padded ranks are read too); many rows by moving x, base and y (4096 rows
+// through qkv, rank 16, in 54 us, 3.0 TB/s: two launches, of which the first reads x at what the L2s give).
 #include "attn_common.h"
 #include "../../include/lora.h"
 
@@ -786,10 +791,13 @@ struct Plan {
 Plan make_plan(int M, int N, int K, int R, int parts) {
     Plan p{};
     const long long cus = w4h::cu_count(), k_units = (K + kUnit - 1) / kUnit;
+    // Tiles of 64 rows in the first product read A less often, tiles of 16 are four times as many workgroups (40 drawn shapes
+    // of 257 to 1024 rows, geometric means: 22.9 us with this bound, 23.9 with 256, 22.5 with 1024).
     const bool many = M > 512;
     p.tiles = (M + kRows - 1) / kRows;
     p.rs = R <= 32 ? 1 : R <= 64 ? 2 : R <= 128 ? 4 : 8;
-    // One launch where a workgroup's read of a (R K x 2 bytes) costs less than a second launch, for one tile of rows: its LDS fills a CU.
+    // One launch where a workgroup's read of all of a part's a costs less than a second launch, for one tile of rows: its LDS
+    // fills a CU.  (R K = 80000: one launch 8 to 11 us, two 11; 120000: 11 to 13 and 10 to 14; 235000: 14.2 and 12.1; 600000: 28 and 15.)
     p.split = M > kRows || (long long)R * K > 100000 || p.rs > 2;
     const int rows = p.split ? parts * R : R;            // of a that a workgroup multiplies
     p.rk = rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 48 && p.split ? 3 : 4;
@@ -798,6 +806,7 @@ Plan make_plan(int M, int N, int K, int R, int parts) {
     const long long least = 4 * kGroup;                  // columns of a block: a group for each of four waves at least
     p.slices = 1;
     if (p.split && M > 64 && p.rs <= 2) {
+        // (64 rows of 48 adapters through gate/up: 47.9 us like this, 34.9 like below; 60 drawn shapes of 65 to 512 rows: 20.8 and 21.7.)
         // By runs of row tiles, the fewest with which all workgroups are on the GPU at once, two per
         // CU; where one-tile runs leave places, several workgroups share a tile's adapters.
         p.cols = (int)least;

@@ -1,5 +1,12 @@
 // rope_append.hip -- rotary positions, and keys and values appended to a paged
-// cache, in one pass over the rows of a fused qkv product.
+// cache, in one pass over the rows of a fused qkv product: pair (x, y) of a query or key
+// head at position p becomes (x c - y s, y c + x s), c and s the cosine and sine of p f.
+//
+// Bound by memory: 64 operations for 32 bytes read and written.  8192 tokens of 40 query and
+// 8 key/value heads of 128 (235 MB) take 48.8 us, 4.8 TB/s; a plain copy reaches 5.2.  One
+// token takes 2.4 us in a graph, a launch's time.  So nothing is read twice, accesses are 16
+// bytes wide and all of a thread's are on their way before the first is used; the sines, 64-bit work, are
+// made once per token and not once per head.
 #include <math.h>
 
 #include "w8a8_common.h"
@@ -11,7 +18,9 @@ namespace {
 
 constexpr int kMaxD = 512;
 constexpr int kMaxThreads = 1024;
-constexpr long long kManyThreads = 1 << 20;   // with a thread for each 16 elements: from here on a thread takes four heads
+// With a thread for each 16 elements: from here on a thread takes four heads, whose loads it has in flight
+// together (40/8 heads of 128, 1024 tokens: 6.8 us with four, 6.2 with one; 2048: 9.4, 10.3; 4096: 20.0, 20.7).
+constexpr long long kManyThreads = 3 << 18;
 
 struct RopeArgs {
     const uint16_t* q;
