@@ -284,9 +284,10 @@ struct Second {
 #pragma unroll
         for (int i = 0; i < 4; ++i) y_row[i] = (r.members >> (4 * g + i)) & 1u ? (uint32_t)((4 * g + i) * a.ldy + 8 * c) * kSize : kNowhere;
         b = a.b + (size_t)max(r.id, 0) * a.N * a.R;
-        // Load j of a step takes columns 16 j .. 16 j + 15, four lanes each; chunk p ^ (column / 8 % 4) goes to place p.
+        // Load j of a step fills places 16 j .. 16 j + 15, four lanes each.  Column q has place q ^ (q / 8 % 4), and there
+        // chunk p of its 32 ranks lies at p ^ (q / 32): lane (c, g)'s reads of columns 8 c + t are spread over all banks.
 #pragma unroll
-        for (int j = 0; j < 2; ++j) b_row[j] = 16u * ((lane & 3) ^ (2 * j + (lane >> 5)));
+        for (int j = 0; j < 2; ++j) b_row[j] = (uint32_t)((lane >> 2) ^ (2 * j + (lane >> 5))) * row_bytes;
     }
     __device__ __forceinline__ uint32_t place(int n, int i) const { return n + 8 * c < n1 ? y_row[i] + (uint32_t)n * kSize : kNowhere; }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t columns(int n) const {
@@ -298,8 +299,8 @@ struct Second {
         const __amdgpu_buffer_rsrc_t rb = columns(n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t chunk = b_row[j & 1] + 64u * s;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(to + 1024 * j), 16, chunk < 2u * r.rank ? (16 * j + (lane >> 2)) * row_bytes + chunk : kNowhere, 0, 0, 0);
+            const uint32_t chunk = 16u * ((lane & 3) ^ (j >> 1)) + 64u * s;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(to + 1024 * j), 16, chunk < 2u * r.rank ? 16 * j * row_bytes + b_row[j & 1] + chunk : kNowhere, 0, 0, 0);
         }
     }
     __device__ __forceinline__ void load_base(u32x4_t (*base)[kWords], int n) const {
@@ -320,7 +321,7 @@ struct Second {
     // Tile t's column 8 c + t of ranks 8 g .. of the step that lies at `from`.
     __device__ __forceinline__ void read_b(const uint8_t* from, u32x4_t* w) const {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) w[t] = *(const u32x4_t*)(from + (8 * c + t) * (2 * kStep) + 16 * (g ^ (c & 3)));
+        for (int t = 0; t < 8; ++t) w[t] = *(const u32x4_t*)(from + ((8 * c + t) ^ (c & 3)) * (2 * kStep) + 16 * (g ^ (c >> 2)));
     }
     __device__ static __forceinline__ void result(const float4_t* acc, const u32x4_t (*base)[kWords], const float* f, u32x4_t (*out)[kWords]) {
 #pragma unroll

@@ -11,7 +11,8 @@
  *   y[m][n]    = base[m][n] + s sum_{j < r} b[a][n][j] h[m][p(n)][j]
  *
  * A row whose adapter is outside 0 .. n_adapters - 1 (-1: none) gets y = base.
- * Rows of one adapter may lie anywhere in the batch.
+ * Rows of one adapter may lie anywhere in the batch; in large batches they cost less side by side (an adapter is
+ * read again by every tile of 16 or 64 rows that uses it).
  *
  * Statuses, dtypes, streams, ownership, capture and workspaces are those of
  * w4a16.h: device pointers 16-byte aligned (ranks, scales and adapter need their own
