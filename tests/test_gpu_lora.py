@@ -232,3 +232,11 @@ def test_after_the_shared_projection():
     c.call()
     want, tol = c.reference()
     assert torch.all((c.g["out"].cpu().double() - want).abs() <= tol)
+
+
+@pytest.mark.parametrize("M,K,R", [(14, 200, 16), (40, 4000, 40), (130, 200, 24), (600, 72, 16), (600, 72, 72)])
+def test_more_than_64_adapters(M, K, R):
+    n = 200
+    ids = [(i * 37 + 60) % (n + 1) - 1 for i in range(M)]
+    c = Case(M, K, [136], R, n, "bf16", "bf16", "own", ids=ids, ranks=[i * 5 % (R + 1) for i in range(n)], seed=M).to_gpu()
+    c.check(c.call())
