@@ -753,6 +753,9 @@ struct Plan {
 Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len) {
     const double kStart = 4.0, kMerge = 4.0, kBytesPerUs = 5.5e6, kPartBytesPerUs = 4.5e6;
     const double own_step = D == 64 ? 0.9 : D == 128 ? 2.2 : 3.5, prefix_step = D == 64 ? 0.7 : D == 128 ? 1.15 : 1.6;
+    // Heads of 256 start late (a block of rows for itself on a CU, nothing beside it; 6 requests of 7 drafts
+    // behind 682 keys: 24.4 us shared, 19.6 each for itself).
+    const double prefix_start = D == 256 ? 11.0 : kStart;
     const int G = Hq / Hkv, R = T * G;
     const long long places = (long long)w4h::cu_count() * (D == 256 ? 1 : 2);
     const long long ptiles = ((long long)max_prefix + kTile - 1) / kTile, otiles = ((long long)max_len + T + kTile - 1) / kTile;
@@ -789,7 +792,7 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len
                 const long long merge_rows = (long long)p.run * T * Hq;
                 if ((p.prefix_groups + p.own_groups) * 8 * 256 > kMaxLanes || (parts > 1 && merge_rows * 256 > kMaxLanes)) continue;
                 const double np = (double)Hkv * p.SP * p.RB, no = (double)p.run * Hkv * SO * p.RO;
-                const double dp = shared ? kStart + ceil((double)ptiles / SP) * prefix_step : 0;
+                const double dp = shared ? prefix_start + ceil((double)ptiles / SP) * prefix_step : 0;
                 const double turns = (double)tiles / SO / kWaves, dn = kStart + 0.5 * (turns + ceil(turns)) * own_step * p.rt;
                 p.own_first = dn > dp;
                 // The longer kind in whole rounds, the shorter one in the places that are left.
