@@ -61,7 +61,8 @@ struct LoraArgs {
 struct Rows {
     int m0;          // the tile's first row
     int id;          // adapter, -1: none
-    int rank;        // rounded up to a multiple of 8
+    int ranks;       // the adapter's
+    int rank;        // rounded up to a multiple of 8: what is read of it
     float scale;
     uint64_t members;
 };
@@ -196,7 +197,8 @@ __device__ __forceinline__ void terms_of(float v0, float v1, uint32_t* term) {
     }
 }
 
-// s h in NT terms of the dtype: hb [term][16][stride], ranks past the adapter's are zeros.
+// s h in NT terms of the dtype: hb [term][16][stride], ranks past the adapter's are zeros (a row with an
+// infinity has NaN there, of the infinity times the zeros that fill a's rank up to eight).
 template <bool BF16, int NT>
 __device__ __forceinline__ void split_h(const LoraArgs& a, const Rows& r, const float* hf, uint16_t* hb, int stride, float* back) {
     const int row = threadIdx.x >> 4, l = threadIdx.x & 15;
@@ -205,14 +207,14 @@ __device__ __forceinline__ void split_h(const LoraArgs& a, const Rows& r, const 
         float up = 1.f;
         if constexpr (!BF16) {
             uint32_t top = 0;
-            for (int j = l; j < r.rank; j += 16) top = max(top, magnitude(src[j] * r.scale));
+            for (int j = l; j < r.ranks; j += 16) top = max(top, magnitude(src[j] * r.scale));
             float down;
             up = to_range(top, down);
             if (l == 0) back[row] = down;
         }
         for (int j = 2 * l; j < stride - 8; j += 32) {
             uint32_t term[NT];
-            terms_of<BF16, NT>(j < r.rank ? src[j] * r.scale * up : 0.f, j + 1 < r.rank ? src[j + 1] * r.scale * up : 0.f, term);
+            terms_of<BF16, NT>(j < r.ranks ? src[j] * r.scale * up : 0.f, j + 1 < r.ranks ? src[j + 1] * r.scale * up : 0.f, term);
 #pragma unroll
             for (int n = 0; n < NT; ++n) *(uint32_t*)(hb + (n * kRows + row) * stride + j) = term[n];
         }
@@ -236,7 +238,7 @@ __device__ __forceinline__ void each_adapter(const LoraArgs& a, int tile, int tu
         const uint64_t same = __builtin_amdgcn_ballot_w64(there && id == one);
         left &= ~same;
         if (i % turns != turn) continue;
-        Rows r{m0, one, 0, 1.f, same};
+        Rows r{m0, one, 0, 0, 1.f, same};
         if (one >= 0) {
             int rank = __builtin_amdgcn_readlane(rank64, one & 63);
             r.scale = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(scale64), one & 63));
@@ -244,7 +246,8 @@ __device__ __forceinline__ void each_adapter(const LoraArgs& a, int tile, int tu
                 rank = a.ranks ? a.ranks[one] : a.R;
                 r.scale = a.scales ? a.scales[one] : 1.f;
             }
-            r.rank = (min(max(__builtin_amdgcn_readfirstlane(rank), 0), a.R) + 7) & ~7;
+            r.ranks = min(max(__builtin_amdgcn_readfirstlane(rank), 0), a.R);
+            r.rank = (r.ranks + 7) & ~7;
         }
         f(r);
     }
@@ -639,7 +642,7 @@ __global__ __launch_bounds__(256, 2) void lora_rows_kernel(LoraArgs a) {
             rank[k] = a.ranks ? a.ranks[max(who[k], 0)] : a.R, scale[k] = a.scales ? a.scales[max(who[k], 0)] : 1.f;
         }
 #pragma unroll
-        for (int k = 0; k < T; ++k) rank[k] = who[k] < 0 ? 0 : (min(max(rank[k], 0), a.R) + 7) & ~7;
+        for (int k = 0; k < T; ++k) rank[k] = who[k] < 0 ? 0 : min(max(rank[k], 0), a.R);
 #pragma unroll
         for (int k = 0; k < T; ++k) {
             if (i0 + k >= tiles) continue;
@@ -648,7 +651,7 @@ __global__ __launch_bounds__(256, 2) void lora_rows_kernel(LoraArgs a) {
             float up = 1.f, down = 1.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                v[k][j] = 4 * l < rank[k] ? v[k][j] * scale[k] : 0.f;   // ranks past the adapter's were not written
+                v[k][j] = 4 * l + j < rank[k] ? v[k][j] * scale[k] : 0.f;   // ranks past the adapter's are zeros times x, or were not written
                 top = max(top, magnitude(v[k][j]));
             }
             if constexpr (!BF16) up = to_range(top, down);
