@@ -353,9 +353,10 @@ struct Second {
 #pragma unroll
             for (int e = 0; e < kWords; ++e) __builtin_amdgcn_raw_buffer_store_b128(out[i][e], ry, place(n, i), 16 * e, 0);
     }
+    // Rows without an adapter: their sum, 0, is taken times -1, as base + 0 would lose the sign of a base of -0.
     __device__ __forceinline__ void scales(const float* back, float* f) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = BF16 ? 1.f : back[4 * g + i];
+        for (int i = 0; i < 4; ++i) f[i] = r.id < 0 ? -1.f : BF16 ? 1.f : back[4 * g + i];
     }
 
     // At most 32 RS ranks, a group or two for a wave: b straight to registers, asked for before h is made.
@@ -715,9 +716,9 @@ __global__ __launch_bounds__(256, 2) void lora_rows_kernel(LoraArgs a) {
                 put(acc, (uint32_t)same);
             }
             const uint64_t none = __builtin_amdgcn_ballot_w64(mine == -1);
-            if (none && turn == 0 && a.base != a.y) {   // base copied
+            if (none && turn == 0 && a.base != a.y) {   // base copied, the sign of -0 too
 #pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k] = float4_t{0.f, 0.f, 0.f, 0.f};
+                for (int k = 0; k < 8; ++k) acc[k] = float4_t{-0.f, -0.f, -0.f, -0.f};
                 put(acc, (uint32_t)none);
             }
             load_base(slot, i + D);

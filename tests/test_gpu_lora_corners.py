@@ -30,3 +30,18 @@ def test_an_infinite_sum_of_any_rank_is_infinite(name, dtype):
     out = c.to_gpu().call().cpu()
     assert form() == name.split(",")[0]
     assert torch.all(torch.isposinf(out[1:3])) and torch.all(torch.isfinite(out[3:])) and torch.all(torch.isfinite(out[0]))
+
+
+@pytest.mark.parametrize("y", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("name", FORMS)
+def test_a_row_without_an_adapter_is_its_base(name, y):
+    M, K, R = FORMS[name]
+    c = Case(M, K, [64, 40], R, 2, "bf16" if y == "f32" else y, y, "own", ids=[i % 3 - 1 for i in range(M)], seed=6)
+    c.base[:, ::3] = -0.0
+    c.base[:, 1::3] = 0.0
+    c.base[::3, 5] = torch.finfo(TYPES[y]).smallest_normal / 4
+    c.base[::3, 8] = float("-inf")
+    out = c.to_gpu().call().cpu()
+    assert form() == name.split(",")[0]
+    bits = torch.int32 if y == "f32" else torch.int16
+    assert torch.equal(out[::3].contiguous().view(bits), c.base[::3].contiguous().view(bits))
