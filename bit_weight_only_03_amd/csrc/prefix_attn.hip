@@ -110,6 +110,52 @@ __device__ __forceinline__ int share(int n, int s, int i) {
     return i * each + min(i, n - s * each);
 }
 
+// An infinity among the values that a row sees makes its column infinite however small its
+// probability, but the products (and the weights of parts and waves) make NaN of an infinity times 0.  So columns
+// d .. d + N - 1 of a row that came out as NaN, its probabilities being numbers, are settled by the values
+// themselves: NaN where there is a NaN or both infinities, else the infinity.  Seldom, and slow: up to all keys are read
+// again (a NaN at the prefix's end that 40960 rows of 16384 keys see: 59 ms; one that 448 x 8 rows of 4099 see: 1.9).
+template <bool BF16, int N>
+__device__ __forceinline__ void settle(const PrefixArgs& a, size_t tok, uint32_t kvh, int d, float* v) {
+    const uint32_t b = tok / (uint32_t)a.T;
+    const int P = min(max(a.prefix_len[0], 0), a.max_prefix), len = min(max(a.lens[b], 0), a.max_len), page_mask = (1 << a.page_shift) - 1;
+    const uint64_t see = a.mask[tok] & (~0ull >> (64 - a.T));
+    uint32_t seen[N];   // bit 0: +infinity, 1: -infinity, 2: NaN
+#pragma unroll
+    for (int i = 0; i < N; ++i) seen[i] = 0;
+#pragma unroll 1
+    for (int own = 1; own >= 0; --own) {   // the shorter first: a NaN ends it
+        const int n = own ? len + a.T : P;
+        const int* const table = own ? a.table + (size_t)b * a.table_stride : a.prefix_table;
+#pragma unroll 1
+        for (int p0 = 0; p0 < n; p0 += 8) {
+            uint16_t x[8][N];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int p = min(p0 + j, n - 1), page = min(max(table[p >> a.page_shift], 0), a.num_pages - 1);
+                const uint16_t* const at = a.v + (long long)page * a.page_stride + (long long)(p & page_mask) * a.token_stride + kvh * a.head_stride + d;
+                __builtin_memcpy(x[j], __builtin_assume_aligned(at, 2 * N), 2 * N);
+            }
+            bool open = false;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int p = min(p0 + j, n - 1);
+                    const float y = unpack1<BF16>(x[j][i]);
+                    const bool sees = !own || p < len || ((see >> (p - len)) & 1);
+                    if (sees && not_finite<BF16>(x[j][i])) seen[i] |= y != y ? 4u : y > 0.f ? 1u : 2u;
+                }
+                open |= v[i] != v[i] && seen[i] < 3u;
+            }
+            if (!__builtin_amdgcn_ballot_w64(open)) return;   // NaN, all that are left
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (v[i] != v[i] && (seen[i] == 1u || seen[i] == 2u)) v[i] = seen[i] == 1u ? __builtin_inff() : -__builtin_inff();
+}
+
 // ------------------------------------------------------------- prefix work
 
 // Workgroup (unit, rb): keys [tile t0, tile t1) of the prefix for kv head unit / SP, rows rb * 128 .. of the B T G.
@@ -597,6 +643,14 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
         float4_t v = *(const float4_t*)from;
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) v += *(const float4_t*)(from + (size_t)w * kRows * kPitch);
+        if (direct && (v[0] != v[0] || v[1] != v[1] || v[2] != v[2] || v[3] != v[3])) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) sum += ml[(w * kRows + e / D) * 2 + 1];
+            float y[4] = {v[0], v[1], v[2], v[3]};
+            if (sum - sum == 0.f) settle<BF16, 4>(a, (size_t)b * a.T + row / G, kvh, e % D, y);
+            v = float4_t{y[0], y[1], y[2], y[3]};
+        }
         if (direct)
             *(u32x2_t*)(a.out + out_row(row) * D + e % D) = u32x2_t{pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3])};
         else
@@ -690,6 +744,10 @@ __global__ __launch_bounds__(256) void prefix_merge_kernel(PrefixArgs a) {
         }
     }
     if (!there || w != 0) return;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < C; ++i) odd |= v[i] != v[i];
+    if (odd && sum - sum == 0.f) settle<BF16, C>(a, row / (uint32_t)a.Hq, (uint32_t)(row % (uint32_t)a.Hq) / (uint32_t)a.G, lane * C, v);
     const float f = sum == 0.f ? 0.f : 1.0f / sum;
     uint16_t* const to = a.out + row * D + lane * C;
     if constexpr (C == 1) {

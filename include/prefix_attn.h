@@ -16,7 +16,8 @@
  *
  * The prefix is multiplied once for the rows of all requests together.  A row that
  * sees nothing (no prefix, no context, an empty mask) gets out = 0 and lse = -infinity.  What a
- * row does not see has no influence on it, NaN and infinity included.
+ * row does not see has no influence on it, NaN and infinity included.  An infinity in the values
+ * that it sees makes its column infinite however small its probability (both infinities, or a NaN: NaN).
  *
  * Statuses, dtypes, streams, ownership, capture and workspaces are those of
  * w4a16.h: device pointers 16-byte aligned (the tables, lengths and tree_mask need
