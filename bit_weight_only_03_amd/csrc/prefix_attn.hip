@@ -68,6 +68,23 @@ constexpr float kLift = BF16 ? 0.f : 12.f;
 template <bool BF16>
 constexpr float kSlack = BF16 ? 8.f : 3.f;
 
+// A score's product with scale2 enters the exponent unrounded, the maximum rounded: past kFar (log2 units) that
+// difference could pass f16's range (and from 2^31 on bf16's).  There every tile rounds each product like the
+// maximum first, so that the largest one's exponent is kLift again.
+constexpr float kFar = 0x1p20f;
+__device__ __forceinline__ bool is_far(float m) { return __builtin_fabsf(m) > kFar && m != -__builtin_inff(); }
+// What a score has to pass for the maximum m to be raised.
+template <bool BF16>
+__device__ __forceinline__ float limit_of(float m) {
+    return __builtin_fabsf(m) > kFar ? -__builtin_inff() : m + kSlack<BF16>;
+}
+template <bool BF16>
+__device__ __forceinline__ float far_exponent(float x, float scale2, float m) {
+#pragma clang fp contract(off)
+    const float y = x * scale2;
+    return y - (m == -__builtin_inff() ? 0.f : m) + kLift<BF16>;
+}
+
 typedef float float16_t __attribute__((ext_vector_type(16)));
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
 
@@ -212,7 +229,7 @@ __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, 
         }
     };
     float16_t o[NT];
-    float m = -__builtin_inff(), l = 0.f;
+    float m = -__builtin_inff(), l = 0.f, limit = m, base = 0.f;   // base: of the exponents, m - kLift
 #pragma unroll
     for (int d = 0; d < NT; ++d)
 #pragma unroll
@@ -287,20 +304,26 @@ __device__ __forceinline__ void prefix_work(const PrefixArgs& a, uint32_t unit, 
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = __builtin_fmaxf(top, x[i]);
         const float mn = max2(top) * a.scale2;
-        if (__builtin_amdgcn_ballot_w64(mn > m + kSlack<BF16>)) {
+        float factor = a.scale2, less = base;
+        if (__builtin_amdgcn_ballot_w64(mn > limit)) {
             const float up = __builtin_fmaxf(m, mn), f = weight_of(m, up);
             l *= f;
 #pragma unroll
             for (int d = 0; d < NT; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[d][i] *= f;
-            m = up;
+            m = up, limit = limit_of<BF16>(m);
+            less = base = m == -__builtin_inff() ? 0.f : m - kLift<BF16>;
+            if (__builtin_amdgcn_ballot_w64(is_far(m))) {
+                factor = 1.f, less = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = far_exponent<BF16>(x[i], a.scale2, m);
+            }
         }
-        const float base = m == -__builtin_inff() ? 0.f : m - kLift<BF16>;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.scale2, -base));
+            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], factor, -less));
             sum += x[i];
         }
         l += sum;   // this lane's keys; the two lanes of a row are added at the end
@@ -410,10 +433,10 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
         for (int s = 0; s < KS; ++s) qf[rt][s] = *(const u32x4_t*)(qp + 32 * s + 8 * g) ^ a.q_sign;
     }
     float4_t o[RT][DT];
-    float m[RT], l[RT];
+    float m[RT], l[RT], limit[RT], base[RT];   // base: of the exponents, m - kLift
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = -__builtin_inff(), l[rt] = 0.f;
+        m[rt] = limit[rt] = -__builtin_inff(), l[rt] = base[rt] = 0.f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[rt][d] = float4_t{0.f, 0.f, 0.f, 0.f};
     }
@@ -501,20 +524,26 @@ __device__ __forceinline__ void own_work(const PrefixArgs& a, uint32_t id, uint3
 #pragma unroll
             for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, x[i]);
             const float mn = max4(top) * a.scale2;
-            if (__builtin_amdgcn_ballot_w64(mn > m[rt] + kSlack<BF16>)) {
+            float factor = a.scale2, less = base[rt];
+            if (__builtin_amdgcn_ballot_w64(mn > limit[rt])) {
                 const float up = __builtin_fmaxf(m[rt], mn), f = weight_of(m[rt], up);
                 l[rt] *= f;
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) o[rt][d][q] *= f;
-                m[rt] = up;
+                m[rt] = up, limit[rt] = limit_of<BF16>(up);
+                less = base[rt] = up == -__builtin_inff() ? 0.f : up - kLift<BF16>;
+                if (__builtin_amdgcn_ballot_w64(is_far(up))) {
+                    factor = 1.f, less = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = far_exponent<BF16>(x[i], a.scale2, up);
+                }
             }
-            const float base = m[rt] == -__builtin_inff() ? 0.f : m[rt] - kLift<BF16>;
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], a.scale2, -base));
+                x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], factor, -less));
                 sum += x[i];
             }
             l[rt] += sum;

@@ -8,7 +8,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
 import bit_weight_only_03_amd as L  # noqa: E402
-from test_gpu_prefix_attn import Case  # noqa: E402
+from test_gpu_prefix_attn import Case, UT  # noqa: E402
 
 INF = float("inf")
 
@@ -87,3 +87,40 @@ def test_a_draft_s_infinity_beside_a_far_larger_score(name, dtype):
     assert torch.all(torch.isneginf(g[:, 1, :, 9]))
     g[:, 1, :, 9] = w[:, 1, :, 9]
     assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("name", SHAPES)
+def test_scores_whose_spacing_in_32_bits_is_large(name, D, dtype, sign):
+    # Sums that are exact in 32 bits, multiples of 2^23 (f16) or 2^40 about 2^29 or 2^50: whatever the rounding of a score, the
+    # largest takes all, and equal ones share.  out: the mean of the values at the largest scores, whose sum is fp32 and
+    # which is rounded once (probabilities are 1); lse: the largest score, to two roundings and its factor's.
+    P, max_prefix, lens = SHAPES[name]
+    c = case(D, dtype, P, lens, seed=D + 1)
+    top = 14 if dtype == "f16" else 20
+    g = torch.Generator().manual_seed(7)
+    c.scale = float(sign)
+    c.q[:] = 2.0 ** top
+    for k in [c.prefix[0]] + [d[0] for d in c.dense]:
+        k.zero_()
+        k[..., 0] = torch.randint(-40, 41, k.shape[:2], generator=g).to(k.dtype) * 2.0 ** (9 if dtype == "f16" else top)
+        k[..., 1] = -(2.0 ** (15 if dtype == "f16" else 30))          # all scores far below zero, or far above
+    c.store()
+    out, lse = c.run(max_prefix=max_prefix)
+    check_form(name)
+    out, lse = out.view(c.B, c.T, c.Hq, D).cpu().double(), lse.view(c.B, c.T, c.Hq).cpu().double()
+    for b in range(c.B):
+        here = int(c.lens[b])
+        k, v = (torch.cat([c.prefix[i], c.dense[b][i]]).double() for i in range(2))
+        for i in range(c.T):
+            see = torch.ones(P + here + c.T, dtype=torch.bool)
+            see[P + here:] = torch.tensor([bool(int(c.mask[b, i]) >> j & 1) for j in range(c.T)])
+            for h in range(c.Hq):
+                a = (k[see, h // 2] @ c.q[b * c.T + i, h * D:(h + 1) * D].double()) * sign
+                at = a == a.max()
+                want = v[see, h // 2][at].mean(0)
+                tol = 2 * UT[dtype] * v[see, h // 2][at].abs().mean(0) + 2.0 ** -24
+                assert torch.all((out[b, i, h] - want).abs() <= tol), (L.w4a16_last_variant(), b, i, h)
+                assert abs(lse[b, i, h] - a.max()) <= 2.0 ** -21 * a.max().abs()
