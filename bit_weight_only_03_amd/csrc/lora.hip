@@ -790,7 +790,7 @@ struct Plan {
     int first_threads, threads, turns, first_turns, first_groups, cols, slices;
     int run;              // row tiles of a workgroup of the second launch; 0: not by runs
     long long tiles, first_tiles;
-    size_t ws;
+    size_t ws;            // for this many rows and any fewer
 };
 
 Plan make_plan(int M, int N, int K, int R, int parts) {
@@ -842,7 +842,19 @@ Plan make_plan(int M, int N, int K, int R, int parts) {
         const long long spare = cus / (p.first_tiles * p.first_groups * p.slices);
         const int some = many ? 1 : kRows / 4;
         p.first_turns = M < kRows ? M : M <= 64 || spare >= kRows ? kRows : spare > some ? (int)spare : some;
-        p.ws = w4h::ws_bytes((size_t)p.slices * M * parts * R * sizeof(float));
+        // More rows take fewer slices: the workspace is for the most rows of partial sums that M rows or fewer
+        // have, so that the largest batch's serves every smaller one.  A launch of one workgroup a row, of two
+        // for 16 and of one for 64 rows has at most cus workgroups as soon as it has two slices.
+        long long most = M;
+        auto up_to = [&](long long m, long long rows_of_one, long long units) {
+            const long long on_all = rows_of_one * cus / p.first_groups, sliced = (units < 16 ? units : 16) * (m < M ? m : M);
+            const long long here = on_all < sliced ? on_all : sliced;
+            most = most > here ? most : here;
+        };
+        up_to(64, 1, k_units / 16);
+        if (M > 64) up_to(512, 8, k_units / 16);
+        if (many) up_to(M, 64, k_units / 8);
+        p.ws = w4h::ws_bytes((size_t)most * parts * R * sizeof(float));
     }
     return p;
 }

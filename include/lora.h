@@ -48,7 +48,7 @@ extern "C" {
  * Other than base = y nothing overlaps.
  * Shape: 1 <= M <= 2^26, N >= 8, N % 8 == 0, N <= 2^24, 8 <= K <= 2^20, K % 8 == 0, ldx <= 2^24, ldy <= 2^25,
  * R a multiple of 8 up to 256, 1 <= n_adapters, 1 <= parts <= 4.  workspace may be NULL where the query
- * reports 0.  Both calls return W4A16_ERR_UNSUPPORTED where a launch would need 2^32 work-items. */
+ * reports 0; what it reports for M rows (the other sizes the same) is enough for any fewer.  Both calls return W4A16_ERR_UNSUPPORTED where a launch would need 2^32 work-items. */
 int lora_workspace_bytes(int M, int N, int K, int R, int parts, size_t* bytes);
 int lora_add(const void* x, int dtype, long long ldx, const void* a, const void* b,
              const int32_t* ranks, const float* scales, int n_adapters, const int32_t* adapter,
