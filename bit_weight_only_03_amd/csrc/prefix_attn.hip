@@ -830,7 +830,6 @@ struct Plan {
     int run;                  // requests of a launch
     long long prefix_groups, own_groups;
     bool own_first;
-    size_t ws;
     bool ok;
 };
 
@@ -849,7 +848,9 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len
     const bool in_l2 = ptiles * kTile * Hkv * D * 4 <= (32LL << 20);
     Plan best{};
     double least = 0;
-    for (int shared = 0; shared <= (max_prefix > 0 ? 1 : 0); ++shared) {
+    // A prefix of one tile is not worth its parts (1024 requests of 32/4 heads of 256, 100 of their own: shared 161 us, read
+    // again by each 129; 4096 of 40/8 heads of 64: 258 and 204; 1024 of 8 heads of 256 without a context: 170 and 175).
+    for (int shared = 0; shared <= (max_prefix > kTile ? 1 : 0); ++shared) {
         const int rt = R <= 16 || D == 256 ? 1 : 2, RO = (R + 16 * rt - 1) / (16 * rt);
         const long long units = (long long)B * Hkv * RO, blocks = (long long)Hkv * (((long long)B * R + kBlockRows - 1) / kBlockRows);
         // Splits worth a look: a few, and those that fill the places once, or what the other kind leaves of them.
@@ -875,7 +876,6 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len
                 p.RB = (int)(((long long)p.run * R + kBlockRows - 1) / kBlockRows);
                 p.prefix_groups = ((long long)Hkv * p.SP + 7) / 8 * p.RB;
                 p.own_groups = ((long long)p.run * Hkv * SO + 7) / 8 * p.RO;
-                p.ws = parts > 1 ? w4h::ws_bytes((size_t)p.run * row) : 0;
                 const long long merge_rows = (long long)p.run * T * Hq;
                 if ((p.prefix_groups + p.own_groups) * 8 * 256 > kMaxLanes || (parts > 1 && merge_rows * 256 > kMaxLanes)) continue;
                 const double np = (double)Hkv * p.SP * p.RB, no = (double)p.run * Hkv * SO * p.RO;
@@ -898,6 +898,17 @@ Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len
     return best;
 }
 
+// The workspace that is asked for: the most that the plans of this shape or of any smaller one (fewer requests, drafts,
+// shorter lengths) can take, since fewer requests take more parts.  The largest batch's workspace then serves all.
+size_t workspace_of(int B, int T, int Hq, int D, int max_prefix, int max_len) {
+    const long long ptiles = ((long long)max_prefix + kTile - 1) / kTile, tiles = ((long long)max_len + T + kTile - 1) / kTile + ptiles;
+    const long long SP = max_prefix > kTile ? (ptiles / 4 < 1 ? 1 : ptiles / 4) : 0, SO = tiles / (2 * kWaves) < 1 ? 1 : tiles / (2 * kWaves);
+    const long long parts = SP + SO < kMaxParts ? SP + SO : kMaxParts;
+    if (parts == 1) return 0;
+    const long long bytes = (long long)B * T * Hq * parts * (D + 2) * 4;
+    return w4h::ws_bytes(bytes < (long long)kMaxPartBytes ? (size_t)bytes : kMaxPartBytes);
+}
+
 int check_shape(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len) {
     if (B < 1 || T < 1 || T > 64 || Hkv < 1 || Hq < Hkv || Hq % Hkv || max_len < 0 || max_len > (1 << 30) || max_prefix < 0 ||
         max_prefix > (1 << 30))
@@ -915,7 +926,7 @@ extern "C" int prefix_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D,
     if (int rc = check_shape(B, T, Hq, Hkv, D, max_prefix, max_len)) return rc;
     const Plan p = make_plan(B, T, Hq, Hkv, D, max_prefix, max_len);
     if (!p.ok) return W4A16_ERR_UNSUPPORTED;
-    *bytes = p.ws;
+    *bytes = workspace_of(B, T, Hq, D, max_prefix, max_len);
     return W4A16_OK;
 }
 
@@ -944,8 +955,9 @@ extern "C" int prefix_attn(const void* q, long long q_stride, const void* k, con
     if (page_size < 16) return W4A16_ERR_UNSUPPORTED;   // a half of a tile lies in one page
     const Plan p = make_plan(B, T, Hq, Hkv, D, max_prefix, max_len);
     if (!p.ok) return W4A16_ERR_UNSUPPORTED;
-    if (p.ws && !workspace) return W4A16_ERR_NULL;
-    if (workspace_bytes < p.ws) return W4A16_ERR_WORKSPACE;
+    const size_t need = workspace_of(B, T, Hq, D, max_prefix, max_len);
+    if (need && !workspace) return W4A16_ERR_NULL;
+    if (workspace_bytes < need) return W4A16_ERR_WORKSPACE;
     PrefixArgs a{};
     a.k = (const uint16_t*)k, a.v = (const uint16_t*)v;
     a.prefix_table = prefix_table, a.prefix_len = prefix_len;

@@ -51,7 +51,8 @@ extern "C" {
  * max_prefix, max_len <= 2^30, table_stride * page_size >= max_len + T.  The maxima bound the
  * lengths (host knowledge: they size the split over the keys; a captured graph stays valid
  * for all lengths up to them).  Deterministic for the same lengths.  workspace may be NULL where the query
- * reports 0; a batch whose partial sums pass 128 MiB is taken in several runs of requests that reuse it.
+ * reports 0; what it reports (at most 128 MiB and the head) is enough for any smaller B, T, max_prefix and max_len
+ * too.  A batch whose partial sums pass 128 MiB is taken in several runs of requests that reuse it.
  * Both calls return W4A16_ERR_UNSUPPORTED for another D, the call for a smaller page_size, and both where a launch
  * would need 2^32 work-items. */
 int prefix_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len,

@@ -53,8 +53,10 @@
  *     again.  The rest is scratch that a call writes before it reads it.  So
  *     one workspace, zeroed once, may serve any sequence of calls of any
  *     entry point and shape on one stream, graph replays included; calls
- *     that may overlap in time need distinct workspaces.  A head that is not
- *     zero gives wrong results (never a fault or a hang: no kernel waits on
+ *     that may overlap in time need distinct workspaces.  Each shape's size
+ *     is asked for (fewer rows or requests may need more than many), except
+ *     where an entry point says that its answer covers smaller ones.  A head
+ *     that is not zero gives wrong results (never a fault or a hang: no kernel waits on
  *     a counter).
  */
 #ifndef W4A16_H

@@ -32,3 +32,22 @@ def test_lora_of_fewer_rows():
                    "        if M <= most: print(lib.lora_add(p, 1, K, p, p, None, None, 1, p, None, p, 1, N, None, 1, M, N, K, R, p, need, None))\n"
                    "    print(lib.lora_add(p, 1, K, p, p, None, None, 1, p, None, p, 1, N, None, 1, most, N, K, R, p, need - 1, None))\n")
     assert got.count(-5) == 3 and set(got) == {-5, -7}, got
+
+
+def test_prefix_attn_of_a_smaller_batch():
+    q = lib.prefix_attn_workspace_bytes
+    sizes = dict(B=(1, 2, 3, 7, 16, 39, 40, 61, 64, 256, 1000, 3000), T=(1, 2, 7, 64), P=(0, 1, 32, 33, 300, 777, 7000, 7500, 8192, 131000, 1 << 30),
+                 L=(0, 31, 100, 300, 480, 700, 1000, 8000, 1 << 30))
+    for Hq, Hkv, D in ((40, 8, 128), (16, 16, 64), (8, 1, 256), (128, 4, 128)):
+        need = {(B, T, P, n): q(B, T, Hq, Hkv, D, P, n) for B in sizes["B"] for T in sizes["T"] for P in sizes["P"] for n in sizes["L"]}
+        for at, (name, v) in enumerate(sizes.items()):
+            up = dict(zip(v, v[1:]))
+            for key, b in need.items():
+                if key[at] in up:
+                    assert b <= need[(*key[:at], up[key[at]], *key[at + 1:])], (key, name)
+    got = statuses("for most, T, P, n in ((64, 1, 8192, 700), (256, 4, 16384, 300), (16, 7, 300, 9000)):\n"
+                   "    need = L.prefix_attn_workspace_bytes(most, T, 40, 8, 128, P, n)\n"
+                   "    call = lambda B, P, n, have: print(lib.prefix_attn(p, 5120, p, p, 1, 1, 16, 0, 128, 0, p, p, P, p, 1000, p, n, p, 0.1, p, None, B, T, 40, 8, 128, p, have, None))\n"
+                   "    [call(B, P // c, n // d, need) for B in (1, 2, 16, 39, 40, 61, 64, 200, 256) if B <= most for c in (1, 2, 50, 1000) for d in (1, 3, 1000)]\n"
+                   "    call(most, P, n, need - 1)\n")
+    assert got.count(-5) == 3 and set(got) == {-5, -7}, got
