@@ -45,7 +45,6 @@ struct LoraArgs {
     void* y;
     float* h;             // [slice][M][parts R], partial sums of the first product
     long long ldx, ldy;
-    int y_dtype;
     int n, M, N, K, R, parts;
     int part_start[LORA_MAX_PARTS + 1];
     int block_start[LORA_MAX_PARTS + 1];   // first column block of each part
@@ -922,7 +921,7 @@ extern "C" int lora_add(const void* x, int dtype, long long ldx, const void* a, 
     if (workspace_bytes < p.ws) return W4A16_ERR_WORKSPACE;
     g.x = (const uint16_t*)x, g.a = (const uint16_t*)a, g.b = (const uint16_t*)b;
     g.ranks = ranks, g.scales = scales, g.adapter = adapter, g.base = base, g.y = y, g.h = (float*)w4h::ws_part(workspace);
-    g.ldx = ldx, g.ldy = ldy, g.y_dtype = y_dtype;
+    g.ldx = ldx, g.ldy = ldy;
     g.n = n_adapters, g.M = M, g.N = N, g.K = K, g.R = R, g.parts = parts;
     g.cols = p.cols, g.turns = p.turns, g.first_turns = p.first_turns, g.slices = p.slices;
     g.first_tiles = (uint32_t)p.first_tiles, g.first_groups = p.first_groups, g.run = p.run;

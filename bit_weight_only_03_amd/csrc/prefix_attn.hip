@@ -839,8 +839,9 @@ struct Plan {
 Plan make_plan(int B, int T, int Hq, int Hkv, int D, int max_prefix, int max_len) {
     const double kStart = 4.0, kMerge = 4.0, kBytesPerUs = 5.5e6, kPartBytesPerUs = 4.5e6;
     const double own_step = D == 64 ? 0.9 : D == 128 ? 2.2 : 3.5, prefix_step = D == 64 ? 0.7 : D == 128 ? 1.15 : 1.6;
-    // Heads of 256 start late (a block of rows for itself on a CU, nothing beside it; 6 requests of 7 drafts
-    // behind 682 keys: 24.4 us shared, 19.6 each for itself).
+    // Heads of 256 start late (a block of rows for itself on a CU, nothing beside it).  Six batches of 1 to 128 requests behind 100
+    // to 32768 keys, both forms measured: the faster one is taken, but for two of the 42 (6 requests of 7 drafts
+    // behind 8192 keys: shared 30 us, each for itself 26; 128 of 2 behind 682: 25 and 22).
     const double prefix_start = D == 256 ? 11.0 : kStart;
     const int G = Hq / Hkv, R = T * G;
     const long long places = (long long)w4h::cu_count() * (D == 256 ? 1 : 2);
