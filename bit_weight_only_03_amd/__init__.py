@@ -413,9 +413,9 @@ def tree_attn(q, q_stride, k, v, dtype, num_pages, page_size, page_stride, token
 
 
 def rope_frequencies(rot_dim: int, base: float, factor=1.0, original=0.0, slow=1.0, fast=32.0) -> list:
-    f = (_F * max(rot_dim // 2, 1))()
-    _check("rope_frequencies", _lib.rope_frequencies(f, rot_dim, base, factor, original, slow, fast))
-    return list(f)
+    f = (_F * 512)()   # the most that a call fills
+    _check("rope_frequencies", _lib.rope_frequencies(f, rot_dim if 0 < rot_dim <= 1024 else 0, base, factor, original, slow, fast))
+    return f[:rot_dim // 2]
 
 
 def rope_append(q, q_stride, k, k_stride, v, v_stride, dtype, positions, inv_freq, rot_dim, interleaved, gain, q_out,

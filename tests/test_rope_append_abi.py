@@ -94,3 +94,10 @@ def test_frequency_refusals():
               (64, 1e4, 2.0, inf), (64, 1e4, 2.0, 4096.0, 0.0, 32.0), (64, 1e4, 2.0, 4096.0, 32.0, 32.0), (64, 1e4, 2.0, 4096.0, 1.0, inf),
               (64, 1e4, 2.0, 4096.0, nan, 32.0)):
         assert s(*a) == -2, a
+
+
+def test_frequencies_of_a_size_past_a_c_int():
+    # Refused, neither cut to 32 bits (which would write past a list made for the number given) nor given room for.
+    for n in (1 << 20, (1 << 32) + 64, 64 - (1 << 32), 1 << 45):
+        assert status(lib.rope_frequencies, n, 1e4) == -2, n
+    assert len(lib.rope_frequencies(1024, 1e4)) == 512
