@@ -15,10 +15,11 @@
 // B and the x of many rows go through LDS, whole lines at a time, in a ring that each wave
 // has for itself: no barriers, only counted waits.
 //
-// Few rows are bound by latency (one token through qkv 5120 -> 7168, rank 16: 7.9 us in a graph; what it
+// Few rows are bound by latency (one token through qkv 5120 -> 7168, rank 16: 8.2 us in a graph; what it
 // reads takes 0.2) and by reading the adapters (64 requests of 48 adapters through gate/up 5120 ->
-// 34816, ranks 8 to 32: 34.9 us, 2.0 TB/s of 69 MB, and padded ranks are read too); many rows by moving x, base and y (4096 rows
+// 34816, ranks 8 to 32: 32 us, 2.2 TB/s of 69 MB, and padded ranks are read too); many rows by moving x, base and y (4096 rows
 // through qkv, rank 16, in 54 us, 3.0 TB/s: two launches, of which the first reads x at what the L2s give).
+// Times are per call with three sets of inputs in turn; the same inputs again, from the caches, take 27 and 42 us.
 #include "attn_common.h"
 #include "../../include/lora.h"
 
@@ -810,7 +811,7 @@ Plan make_plan(int M, int N, int K, int R, int parts) {
     const long long least = 4 * kGroup;                  // columns of a block: a group for each of four waves at least
     p.slices = 1;
     if (p.split && M > 64 && p.rs <= 2) {
-        // (64 rows of 48 adapters through gate/up: 47.9 us like this, 34.9 like below; 60 drawn shapes of 65 to 512 rows: 20.8 and 21.7.)
+        // (64 rows of 48 adapters through gate/up: 45.4 us like this, 32.2 like below; 60 drawn shapes of 65 to 512 rows: 20.8 and 21.7.)
         // By runs of row tiles, the fewest with which all workgroups are on the GPU at once, two per
         // CU; where one-tile runs leave places, several workgroups share a tile's adapters.
         p.cols = (int)least;

@@ -15,9 +15,10 @@
 // LDS by transposing reads (prefix work), or (own work) lane r of operand tile t takes column
 // (D/16) r + t, so that it loads consecutive columns of each key and pairs keys up with byte permutes.
 //
-// Measured: 256 requests of 4 drafts, 40 query heads of 128, over 16384 shared keys in 408 us: 853
-// TFLOP/s, of 1214 that a large library product reaches; the softmax between the products takes the rest.  8 requests behind a
-// document of 131000 keys (8 key/value heads), 1000 of their own, in 95 us: 5.9 TB/s, the cache read once.
+// Measured (a call among others, three sets of inputs in turn, from a graph or not): 256 requests of 4 drafts, 40 query heads
+// of 128, over 16384 shared keys in 406 to 415 us: 840 to 858 TFLOP/s, of 1214 that a large library product reaches; the
+// softmax between the products takes the rest.  8 requests behind a document of 131000 keys (8 key/value heads), 1000 of
+// their own, in 96.5 us: 5.8 TB/s, the cache read once.
 #include "attn_common.h"
 #include "../../include/prefix_attn.h"
 

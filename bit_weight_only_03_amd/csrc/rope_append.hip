@@ -4,7 +4,7 @@
 //
 // Bound by memory: 64 operations for 32 bytes read and written.  8192 tokens of 40 query and
 // 8 key/value heads of 128 (235 MB) take 48.8 us, 4.8 TB/s; a plain copy reaches 5.2.  One
-// token takes 2.4 us in a graph, a launch's time.  So nothing is read twice, accesses are 16
+// token takes 2.8 us in a graph, a launch's time.  So nothing is read twice, accesses are 16
 // bytes wide and all of a thread's are on their way before the first is used; the sines, 64-bit work, are
 // made once per token and not once per head.
 #include <math.h>

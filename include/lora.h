@@ -44,7 +44,8 @@ extern "C" {
  * dtype      W4A16_F16 or W4A16_BF16, of x, a and b.  Products and sums are fp32; h stays fp32
  *            (it enters the second product as a sum of 16-bit terms: 2^-16 of its
  *            largest element at most is left out for a 16-bit y, 2^-21 for an fp32 y).
- * The result is deterministic.  A row with a NaN or an infinity changes no other row.
+ * The result is deterministic.  A row with a NaN or an infinity changes no other row.  An infinity in x or a makes an
+ * infinite sum infinite; b is finite (an infinity there makes its column NaN for its adapter's rows, as h's terms may be 0).
  * Other than base = y nothing overlaps.
  * Shape: 1 <= M <= 2^26, N >= 8, N % 8 == 0, N <= 2^24, 8 <= K <= 2^20, K % 8 == 0, ldx <= 2^24, ldy <= 2^25,
  * R a multiple of 8 up to 256, 1 <= n_adapters, 1 <= parts <= 4.  workspace may be NULL where the query

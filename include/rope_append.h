@@ -35,6 +35,8 @@ extern "C" {
  *   original > 0 (that length): by parts.  A pair that turns n = original f / (2 pi) times
  *     over the length keeps f where n >= fast, gets f / factor where n <= slow, and
  *     f (w + (1 - w) / factor), w = (n - slow) / (fast - slow), between.
+ * The ramp is linear in the turns.  A model with another one (linear in the pair's index, say: single
+ * frequencies differ by up to two fifths) needs its own list, made by its own formula: rope_append takes any.
  * rot_dim even, 2..1024; base > 1, factor >= 1, original >= 0, and 0 < slow < fast
  * where original > 0; all finite. */
 int rope_frequencies(float* inv_freq, int rot_dim, double base, double factor, double original,
@@ -55,7 +57,8 @@ int rope_frequencies(float* inv_freq, int rot_dim, double base, double factor, d
  * interleaved 0 (halves) or 1; gain finite, multiplies c and s; dtype W4A16_F16 or W4A16_BF16.
  * q and q_out may both be NULL (only keys and values: Hq is not looked at); k, v, both caches and slots
  * may all be NULL (only queries: Hkv, the page counts and strides are not).  Not both.  Other than q_out = q nothing overlaps.
- * Shape: M >= 1, D a multiple of 16 up to 512, rot_dim a multiple of 16 up to D, 1 <= Hq, Hkv
+ * Shape: M >= 1, D a multiple of 16 up to 512, rot_dim a multiple of 16 up to D (a thread turns the eight pairs that two
+ * 16-byte pieces of a head hold, so no piece is part turned; 20 or 24 elements are refused), 1 <= Hq, Hkv
  * <= 2^16, page_size a power of two.  A launch of 2^32 work-items (a token takes 64 at
  * least, and about one for each 16 or, of many tokens, 64 elements of its heads) returns
  * W4A16_ERR_UNSUPPORTED. */
